@@ -1,0 +1,96 @@
+// vocab_rows.cuh -- what the operators on rows of logits (top logits, beam selection, distillation) share:
+// row loads, order-preserving keys, and sums of exponentials about a power of two.
+//
+// Sums of exponentials.  With c = log2(e) / T a row's terms are exp(z / T) = 2^(c z).  A partial sum is a
+// pair (n, s) that stands for s * 2^n with n a whole number held in a float: a term is 2^(fma(z, c, -n)),
+// rounded once before the exponential because n is exact, and two partial sums join by an exact scaling
+// with a power of two.  (With the running maximum itself as the reference, c * max is rounded and that
+// rounding, relative 2^-24 of the exponent, enters every rescaling.)  c is rounded to fp32 once;
+// log_sum_exp adds back delta * max for the part delta that it lost, which leaves delta * E_q[max - z].
+#pragma once
+
+#include "common.cuh"
+
+namespace domino {
+
+// Sums take magnitudes above kBig for kBig, so that a masked value of the type's lowest, or an infinity, meets
+// others in 64 bits with 2e-7 to spare at any temperature.  A row whose maximum lies within kPlain needs no
+// clamp: what is below -kBig there has a term below 2^-700.
+constexpr float kBig = 1e6f;
+constexpr float kPlain = 5e5f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float big_clamp(float z) { return fminf(fmaxf(z, -kBig), kBig); }
+
+// Whole-number reference for terms up to the maximum m > -infinity.
+__device__ __forceinline__ float reference_of(float m, float c) { return ceilf(big_clamp(m) * c); }
+
+// 2^(c z - n) for any z: NaN and -infinity have no mass.
+__device__ __forceinline__ float term_guarded(float z, float c, float n) {
+  return z > -INFINITY ? ex2(fmaf(big_clamp(z), c, -n)) : 0.f;
+}
+
+// Whether a row or part of a row with maximum m needs term_guarded throughout.
+__device__ __forceinline__ bool is_extreme(float m) { return !(fabsf(m) <= kPlain); }
+
+struct ExpSum {
+  float n = -INFINITY, s = 0.f;
+};
+
+// Raises the reference of `a` to n (n >= a.n, n finite).
+__device__ __forceinline__ void raise(ExpSum& a, float n) {
+  a.s *= ex2(a.n - n);  // a.n = -infinity: 0
+  a.n = n;
+}
+
+// Order-preserving map of a logit onto 32 bits: larger is larger, -0 equals +0; NaN and -infinity, which
+// are never selected, are 0.
+__device__ __forceinline__ uint32_t order_of(float z) {
+  if (!(z > -INFINITY)) return 0u;
+  uint32_t u = __float_as_uint(z);
+  if (u == 0x80000000u) u = 0u;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+// Selection key: a larger logit first, then the lower column.  Key 0 is none.
+__device__ __forceinline__ uint64_t select_key(uint32_t order, int v) {
+  return order ? (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(v)) : 0ull;
+}
+
+// Block sums and maxima in a fixed order; red has one slot per warp, all threads get the result.
+template <typename F, typename Op>
+__device__ __forceinline__ F block_reduce(F v, F* red, Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  F r = red[0];
+  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) r = op(r, red[w]);
+  return r;
+}
+struct MaxOp {
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+  __device__ double operator()(double a, double b) const { return fmax(a, b); }
+};
+struct AddOp {
+  template <typename F> __device__ F operator()(F a, F b) const { return a + b; }
+};
+
+// log of sum * 2^n (natural), with the correction for c's rounding; m: the row's maximum.
+constexpr double kLn2 = 0.693147180559945309417232;
+constexpr double kLog2e = 1.44269504088896340735992;
+__device__ __forceinline__ double log_sum_exp(double sum, double n, float m, float c, double inv_t) {
+  if (!(sum > 0.0)) return -INFINITY;
+  const double delta = kLog2e * inv_t - (double)c;
+  return kLn2 * (log2(sum) + n + delta * (double)big_clamp(m));
+}
+
+}  // namespace domino

@@ -5,13 +5,16 @@ provides device memory and the current stream.  If ``libdomino.so`` is missing o
 loaded, every call raises -- there is no CPU fallback.
 
 Names follow the C ABI without the ``domino_`` prefix: ``draft_greedy``, ``teacher_forced``,
-``accept_len``, ``workspace_bytes``, ``accept_workspace_bytes``, ``status_string``.
+``accept_len``, ``top_logits``, ``beam_select``, ``distill``, ``workspace_bytes``,
+``accept_workspace_bytes``, ``status_string``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -39,7 +42,8 @@ EXPORTS = ("domino_workspace_bytes", "domino_draft_greedy", "domino_teacher_forc
            "domino_embed_proj_bytes", "domino_project_embeddings", "domino_arena_bytes",
            "domino_pack_weights", "domino_set_l2_persistence", "domino_debug_gemm",
            "domino_debug_read_passes", "domino_teacher_forced_ex", "domino_accept_sample_workspace_bytes",
-           "domino_accept_sample")
+           "domino_accept_sample", "domino_top_logits", "domino_beam_workspace_bytes", "domino_beam_select",
+           "domino_distill", "domino_distill_backward")
 
 
 class DominoError(RuntimeError):
@@ -54,6 +58,21 @@ class Shape(ctypes.Structure):
 
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("embed", "W_ih", "W_hh", "b_ih", "b_hh", "W1", "W2", "embed_proj")]
+
+
+class BeamArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "W_in", "W_out", "V")] + [("ld", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("dtype", "eos", "Hs", "hist_len", "pos")] +
+                [(n, ctypes.c_void_p) for n in ("logits", "scores", "finished", "states", "history", "scores_out",
+                                                "parents_out", "tokens_out", "finished_out", "states_out",
+                                                "history_out")])
+
+
+class DistillArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("V", ctypes.c_int32), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("logits", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+                ("top_logits", ctypes.c_void_p), ("teacher_lse", ctypes.c_void_p), ("row_weights", ctypes.c_void_p),
+                ("temperature", ctypes.c_float)]
 
 
 _lib = None
@@ -118,6 +137,16 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
         L.domino_accept_sample_workspace_bytes.restype = sz
         L.domino_accept_sample.argtypes = [i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp, vp]
         L.domino_accept_sample.restype = ctypes.c_int
+        L.domino_top_logits.argtypes = [i32, i32, ctypes.c_int64, i32, vp, i32, ctypes.c_float, vp, vp, vp, vp]
+        L.domino_top_logits.restype = ctypes.c_int
+        L.domino_beam_workspace_bytes.argtypes = [i32, i32, i32]
+        L.domino_beam_workspace_bytes.restype = sz
+        L.domino_beam_select.argtypes = [ctypes.POINTER(BeamArgs), vp, sz, vp]
+        L.domino_beam_select.restype = ctypes.c_int
+        L.domino_distill.argtypes = [ctypes.POINTER(DistillArgs), vp, vp, vp, ctypes.c_int64, i32, vp, vp]
+        L.domino_distill.restype = ctypes.c_int
+        L.domino_distill_backward.argtypes = [ctypes.POINTER(DistillArgs), vp, vp, vp, ctypes.c_int64, i32, vp, vp]
+        L.domino_distill_backward.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -557,6 +586,277 @@ def accept_sample(draft_tokens, target_logits, temperature: float, uniforms, dra
                  _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream, dev))
     _check(rc, "domino_accept_sample")
     return accept_out, next_out
+
+
+# ---- rows of logits: top logits, beam selection, distillation ----
+
+MAX_TOP = 128
+MAX_BEAMS = 32
+_DTYPE_CODE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _logit_rows(t, name: str):
+    """(leading shape, V, ld, dtype code) of a [..., V] tensor whose rows lie a fixed multiple of 8 values apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2 or 0 in shape:
+        raise ValueError(f"{name} must be a [..., V] tensor with at least one row, not {tuple(shape)}")
+    V = shape[-1]
+    ld = run = None
+    for n, s in zip(shape[-2::-1], strides[-2::-1]):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = run = s
+        elif s != run:
+            raise ValueError(f"the rows of {name} must lie one fixed stride apart")
+        run *= n
+    padded = (V + 7) // 8 * 8
+    if ld is None:  # a single row
+        ld = padded
+    if (strides[-1] != 1 and V > 1) or ld < V or ld % 8:
+        raise ValueError(f"the rows of {name} must be contiguous and a multiple of 8 values apart (stride {ld}, V {V}): "
+                         f"pad the vocabulary's storage")
+    if padded != V:
+        rows = t.numel() // V
+        if (t.storage_offset() + (rows - 1) * ld + padded) * t.element_size() > t.untyped_storage().nbytes():
+            raise ValueError(f"the last row of {name} must be followed by storage up to a multiple of 8 values")
+    return shape[:-1], V, ld, code
+
+
+def _empty_rows(lead, V: int, dtype, device):
+    """An uninitialised [..., V] tensor in rows padded to a multiple of 8 values."""
+    padded = (V + 7) // 8 * 8
+    t = torch.empty(tuple(lead) + (padded,), dtype=dtype, device=device)
+    return t if padded == V else t[..., :V]
+
+
+def _allocating_on(stream):
+    """Memory that a call allocates belongs to the stream it is used on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_out=None, lse_out=None, stream=None):
+    """The k largest of every row of logits [..., V] with their tokens, and the rows' log-sum-exp at ``temperature``
+    (``domino_top_logits``): returns (values [..., k] fp32, ids [..., k] int32, lse [...] fp32).  Logits are fp32 or
+    bf16; descending, the lower token first among equals; id -1 and value -inf where a row has fewer than k."""
+    lead, V, ld, code = _logit_rows(logits, "logits")
+    dev, k = logits.device, int(k)
+    if not 1 <= k <= MAX_TOP:
+        raise ValueError(f"k is {k}, expected 1 to {MAX_TOP}")
+    sp = _stream(stream, dev)
+    with _allocating_on(stream):
+        if values_out is None:
+            values_out = torch.empty(lead + (k,), dtype=torch.float32, device=dev)
+        if ids_out is None:
+            ids_out = torch.empty(lead + (k,), dtype=torch.int32, device=dev)
+        if lse_out is None:
+            lse_out = torch.empty(lead, dtype=torch.float32, device=dev)
+    _expect(values_out, "values_out", lead + (k,), torch.float32, dev)
+    _expect(ids_out, "ids_out", lead + (k,), torch.int32, dev)
+    _expect(lse_out, "lse_out", lead, torch.float32, dev)
+    rc = _launch(dev, lib().domino_top_logits, logits.numel() // V, V, ld, code, logits.data_ptr(), k,
+                 float(temperature), values_out.data_ptr(), ids_out.data_ptr(), lse_out.data_ptr(), sp)
+    _check(rc, "domino_top_logits")
+    return values_out, ids_out, lse_out
+
+
+def beam_workspace_bytes(B: int, W_in: int, W_out: int) -> int:
+    return int(lib().domino_beam_workspace_bytes(int(B), int(W_in), int(W_out)))
+
+
+class BeamStep(NamedTuple):
+    """What beam_select returns; ``states``, ``history`` and ``finished`` are None where they do not apply."""
+    scores: torch.Tensor              # [B, beams] fp32
+    parents: torch.Tensor             # [B, beams] int32
+    tokens: torch.Tensor              # [B, beams] int32
+    states: Optional[torch.Tensor]    # [B, beams, Hs] fp32
+    history: Optional[torch.Tensor]   # [B, beams, hist_len] int32
+    finished: Optional[torch.Tensor]  # [B, beams] uint8
+
+
+def beam_select(logits, scores, beams: int, states=None, history=None, pos: int = 0, finished=None, eos: int = -1,
+                out: "BeamStep | None" = None, workspace=None, stream=None) -> BeamStep:
+    """One step of beam search (``domino_beam_select``): the ``beams`` best continuations of each group by
+    ``scores + log_softmax(logits)``, with states and histories following their parents.
+
+    logits [B, W, V] fp32 or bf16, scores [B, W] fp32 (-inf: a dead beam), states [B, W, Hs] fp32, history
+    [B, W, hist_len] int32 (the token goes to column ``pos``), finished [B, W] uint8 with ``eos``.  ``out`` takes a
+    BeamStep whose tensors are filled; none of them may share memory with an input."""
+    lead, V, ld, code = _logit_rows(logits, "logits")
+    if len(lead) != 2:
+        raise ValueError("logits must be a [B, W, V] tensor")
+    B, W = (int(x) for x in lead)
+    dev, n = logits.device, int(beams)
+    if not (1 <= n <= MAX_BEAMS and W <= MAX_BEAMS):
+        raise ValueError(f"{W} beams to {n}: expected 1 to {MAX_BEAMS}")
+    _expect(scores, "scores", (B, W), torch.float32, dev)
+    Hs = hist_len = 0
+    if states is not None:
+        if not isinstance(states, torch.Tensor) or states.dim() != 3:
+            raise ValueError("states must be a [B, W, Hs] tensor")
+        Hs = int(states.shape[2])
+        _expect(states, "states", (B, W, Hs), torch.float32, dev)
+    if history is not None:
+        if not isinstance(history, torch.Tensor) or history.dim() != 3:
+            raise ValueError("history must be a [B, W, hist_len] tensor")
+        hist_len = int(history.shape[2])
+        _expect(history, "history", (B, W, hist_len), torch.int32, dev)
+    if finished is not None:
+        _expect(finished, "finished", (B, W), torch.uint8, dev)
+    sp = _stream(stream, dev)
+    with _allocating_on(stream):
+        if out is None:
+            out = BeamStep(torch.empty((B, n), dtype=torch.float32, device=dev),
+                           torch.empty((B, n), dtype=torch.int32, device=dev),
+                           torch.empty((B, n), dtype=torch.int32, device=dev),
+                           None if states is None else torch.empty((B, n, Hs), dtype=torch.float32, device=dev),
+                           None if history is None else torch.empty((B, n, hist_len), dtype=torch.int32, device=dev),
+                           None if eos < 0 else torch.empty((B, n), dtype=torch.uint8, device=dev))
+        else:
+            _expect(out.scores, "out.scores", (B, n), torch.float32, dev)
+            _expect(out.parents, "out.parents", (B, n), torch.int32, dev)
+            _expect(out.tokens, "out.tokens", (B, n), torch.int32, dev)
+            for name, given, dims, dt in (("states", states, (B, n, Hs), torch.float32),
+                                          ("history", history, (B, n, hist_len), torch.int32)):
+                t = getattr(out, name)
+                if (t is None) != (given is None):
+                    raise ValueError(f"out.{name} must be given exactly when {name} is")
+                if t is not None:
+                    _expect(t, f"out.{name}", dims, dt, dev)
+            if out.finished is not None:
+                _expect(out.finished, "out.finished", (B, n), torch.uint8, dev)
+        if workspace is None:
+            nbytes = beam_workspace_bytes(B, W, n)
+            if nbytes == 0:
+                raise DominoError(ERR_UNSUPPORTED, "domino_beam_workspace_bytes")
+            workspace = alloc_workspace(nbytes, dev)
+    _expect_workspace(workspace, dev)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    a = BeamArgs(B, W, n, V, ld, code, int(eos), Hs, hist_len, int(pos), logits.data_ptr(), scores.data_ptr(),
+                 ptr(finished), ptr(states), ptr(history), out.scores.data_ptr(), out.parents.data_ptr(),
+                 out.tokens.data_ptr(), ptr(out.finished), ptr(out.states), ptr(out.history))
+    rc = _launch(dev, lib().domino_beam_select, ctypes.byref(a), workspace.data_ptr(), workspace.numel(), sp)
+    _check(rc, "domino_beam_select")
+    return out
+
+
+def _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_weights):
+    """Checks what every distillation call reads; returns (arguments, leading shape, V)."""
+    lead, V, ld, code = _logit_rows(logits, "logits")
+    dev = logits.device
+    if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != len(lead) + 1:
+        raise ValueError("top_ids must be a [..., K] tensor over the rows of logits")
+    K = int(top_ids.shape[-1])
+    if not 1 <= K <= MAX_TOP:
+        raise ValueError(f"{K} entries per row, expected 1 to {MAX_TOP}")
+    _expect(top_ids, "top_ids", lead + (K,), torch.int32, dev)
+    _expect(top_logits, "top_logits", lead + (K,), torch.float32, dev)
+    if teacher_lse is not None:
+        _expect(teacher_lse, "teacher_lse", lead, torch.float32, dev)
+    if row_weights is not None:
+        _expect(row_weights, "row_weights", lead, torch.float32, dev)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    return DistillArgs(logits.numel() // V, V, ld, code, K, logits.data_ptr(), top_ids.data_ptr(),
+                       top_logits.data_ptr(), ptr(teacher_lse), ptr(row_weights), float(temperature)), lead, V
+
+
+def _expect_grad(grad, lead, V, dev):
+    """(ld, dtype code) of a gradient's rows."""
+    glead, gV, gld, gcode = _logit_rows(grad, "grad_out")
+    if glead != lead or gV != V:
+        raise ValueError(f"grad_out has shape {tuple(grad.shape)}, expected {tuple(lead) + (V,)}")
+    if grad.device != dev:
+        raise ValueError(f"grad_out is on {grad.device}, expected {dev}")
+    return gld, gcode
+
+
+def distill(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 1.0, row_weights=None, grad_out=None,
+            loss_out=None, stats_out=None, status=None, stream=None):
+    """Distillation loss of every row of logits [..., V] from a teacher's top logits, and optionally its gradient in
+    the same call (``domino_distill``): returns (loss [...] fp32, grad or None, stats [..., 8] fp32).
+
+    top_ids [..., K] int32 (-1: no entry) and top_logits [..., K] fp32 are what ``top_logits`` gives of the teacher;
+    ``teacher_lse`` [...] fp32 (its third result, at the same temperature) keeps the teacher's remaining mass as one
+    class, without it the entries' probabilities are normalised.  ``row_weights`` [...] fp32 scale the rows' losses
+    (0: the row is skipped).  ``grad_out``: True for a gradient in the logits' type, or a tensor (fp32 or bf16) to
+    fill, which may be ``logits`` itself; it is the gradient of the sum of the losses.  ``stats`` goes to
+    ``distill_backward``."""
+    a, lead, V = _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_weights)
+    dev = logits.device
+    sp = _stream(stream, dev)
+    with _allocating_on(stream):
+        if loss_out is None:
+            loss_out = torch.empty(lead, dtype=torch.float32, device=dev)
+        if stats_out is None:
+            stats_out = torch.empty(lead + (8,), dtype=torch.float32, device=dev)
+        if grad_out is True:
+            grad_out = _empty_rows(lead, V, logits.dtype, dev)
+    if grad_out is False:
+        grad_out = None
+    _expect(loss_out, "loss_out", lead, torch.float32, dev)
+    _expect(stats_out, "stats_out", lead + (8,), torch.float32, dev)
+    _expect_status(status, dev)
+    gptr, gld, gcode = None, 0, 0
+    if grad_out is not None:
+        gld, gcode = _expect_grad(grad_out, lead, V, dev)
+        gptr = grad_out.data_ptr()
+    rc = _launch(dev, lib().domino_distill, ctypes.byref(a), loss_out.data_ptr(), stats_out.data_ptr(), gptr, gld,
+                 gcode, _ptr(status), sp)
+    _check(rc, "domino_distill")
+    return loss_out, grad_out, stats_out
+
+
+def distill_backward(logits, top_ids, top_logits, stats, grad_loss=None, teacher_lse=None, temperature: float = 1.0,
+                     row_weights=None, grad_out=None, status=None, stream=None):
+    """The gradient of ``sum(grad_loss * loss)`` with respect to logits from ``distill``'s arguments and stats
+    (``domino_distill_backward``); grad_loss [...] fp32, None: ones.  ``grad_out`` as in ``distill``."""
+    a, lead, V = _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_weights)
+    dev = logits.device
+    _expect(stats, "stats", lead + (8,), torch.float32, dev)
+    if grad_loss is not None:
+        _expect(grad_loss, "grad_loss", lead, torch.float32, dev)
+    sp = _stream(stream, dev)
+    if grad_out is None or grad_out is True:
+        with _allocating_on(stream):
+            grad_out = _empty_rows(lead, V, logits.dtype, dev)
+    gld, gcode = _expect_grad(grad_out, lead, V, dev)
+    _expect_status(status, dev)
+    rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(),
+                 None if grad_loss is None else grad_loss.data_ptr(), grad_out.data_ptr(), gld, gcode, _ptr(status), sp)
+    _check(rc, "domino_distill_backward")
+    return grad_out
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status):
+        loss, _, stats = distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status=status)
+        ctx.save_for_backward(logits, top_ids, top_logits, teacher_lse, row_weights, stats)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        logits, top_ids, top_logits, teacher_lse, row_weights, stats = ctx.saved_tensors
+        grad = distill_backward(logits, top_ids, top_logits, stats, grad_loss.contiguous(), teacher_lse,
+                                ctx.temperature, row_weights)
+        return grad, None, None, None, None, None, None
+
+
+def distill_loss(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 1.0, row_weights=None,
+                 status=None):
+    """``distill``'s loss as a differentiable function of ``logits``, on the current stream: [...] fp32, one per row.
+    The teacher's tensors and the row weights are constants: one that requires a gradient is refused."""
+    for name, t in (("top_logits", top_logits), ("teacher_lse", teacher_lse), ("row_weights", row_weights)):
+        if isinstance(t, torch.Tensor) and t.requires_grad:
+            raise ValueError(f"{name} requires a gradient, which distill_loss does not give")
+    return _DistillLoss.apply(logits, top_ids, top_logits, teacher_lse, float(temperature), row_weights, status)
 
 
 def to_device_weights(host: dict, dtype_code: int, device="cuda") -> HeadWeights:

@@ -244,6 +244,119 @@ DOMINO_API int domino_accept_sample(int32_t B, int32_t L, int32_t V, const int32
                                     void* workspace, size_t workspace_bytes, int32_t* status_dev,
                                     domino_stream_t stream);
 
+/* ---- Operators on rows of logits: top logits, beam selection, distillation ----
+ *
+ * They read logits as `rows` rows of V values, fp32 or bf16 (`dtype`), `ld` values apart: V may be
+ * any number from 1 to DOMINO_MAX_V and need not be a multiple of 8, but ld must be (ld >= V), the
+ * base must be 16-byte aligned, and V rounded up to a multiple of 8 values must be readable in every
+ * row (what lies there is ignored, and never written).  rows <= DOMINO_MAX_ROWS.
+ *
+ * A logit of -infinity is a barred token: it has no mass and is never selected.  NaN counts as
+ * -infinity.  In sums and scores a magnitude above 1e6 (+infinity, the type's lowest value) counts as
+ * 1e6, so a row of the type's lowest values is a uniform one and a +infinity takes all the mass.
+ * 2^-10 <= temperature <= 2^10 (else DOMINO_ERR_INVALID_ARGUMENT).  Results do not depend on
+ * scheduling: a call repeats bit for bit.  All need compute capability 10.0.  Nothing is launched when
+ * a negative code is returned. */
+#define DOMINO_MAX_V (1 << 20)
+#define DOMINO_MAX_ROWS (1 << 22)
+#define DOMINO_MAX_TOP 128
+#define DOMINO_MAX_BEAMS 32
+
+/* The k largest logits of every row and the row's log-sum-exp -- what a distillation run keeps of the
+ * target model's logits (domino_distill), and the candidates of a draft tree.
+ *   values [rows, k] fp32: descending; ids [rows, k] int32: their columns, the lowest first among equals
+ *   (-0 equals +0); where a row has fewer than k selectable logits the rest is value -infinity, id -1.
+ *   lse [rows] fp32 = log sum_v exp(logits[v] / temperature), -infinity for a row without mass; or NULL.
+ * 1 <= k <= DOMINO_MAX_TOP. */
+DOMINO_API int domino_top_logits(int32_t rows, int32_t V, int64_t ld, int32_t dtype, const void* logits, int32_t k,
+                                 float temperature, float* values, int32_t* ids, float* lse,
+                                 domino_stream_t stream);
+
+/* One step of beam search over B groups of W_in beams: the W_out best continuations of each group, with
+ * the beams' states and histories reordered to follow their parents.
+ *   score(w, v) = scores[b, w] + logits[b, w, v] - log sum_u exp(logits[b, w, u])
+ * computed in 64 bits and ordered by score (descending), then lower beam, larger logit, lower token.
+ * Inputs: logits [B, W_in, V] rows (above); scores [B, W_in] fp32, -infinity (or NaN) for a dead beam,
+ *   which continues nowhere; finished [B, W_in] bytes or NULL: a beam whose byte is not zero has one
+ *   continuation, itself, with token `eos` and its score unchanged (its logits are not read, nor are a
+ *   dead beam's); eos: in [0, V), or -1 for none (finished must then be NULL);
+ *   states [B, W_in, Hs] fp32 (the GRU states; Hs a multiple of 4) or NULL; history [B, W_in, hist_len]
+ *   int32 or NULL, with 0 <= pos < hist_len.
+ * Outputs: scores_out [B, W_out] fp32; parents_out, tokens_out [B, W_out] int32; finished_out [B, W_out]
+ *   bytes (required when finished is given, optional when eos >= 0, else NULL): 1 for a beam that had
+ *   finished or takes eos now; states_out [B, W_out, Hs] = the parent's state; history_out [B, W_out,
+ *   hist_len] = the parent's history with the token at `pos`.  states_out and history_out go with their
+ *   inputs.  Where a group has fewer than W_out continuations the remaining beams are dead: score
+ *   -infinity, parent 0, token 0, finished 0.
+ * No output may overlap an input (DOMINO_ERR_INVALID_ARGUMENT).  1 <= W_in, W_out <= DOMINO_MAX_BEAMS.
+ * Needs domino_beam_workspace_bytes(B, W_in, W_out) bytes of workspace (256-byte aligned). */
+typedef struct {
+  int32_t B, W_in, W_out, V;
+  int64_t ld;
+  int32_t dtype, eos, Hs, hist_len, pos;
+  const void* logits;
+  const float* scores;
+  const uint8_t* finished;
+  const float* states;
+  const int32_t* history;
+  float* scores_out;
+  int32_t *parents_out, *tokens_out;
+  uint8_t* finished_out;
+  float* states_out;
+  int32_t* history_out;
+} domino_beam_t;
+
+DOMINO_API size_t domino_beam_workspace_bytes(int32_t B, int32_t W_in, int32_t W_out);
+DOMINO_API int domino_beam_select(const domino_beam_t* beam, void* workspace, size_t workspace_bytes,
+                                  domino_stream_t stream);
+
+/* Distillation of a row of logits from a teacher's top logits: the loss and its gradient.
+ *   q = softmax(logits / temperature); teacher entry k of a row is token top_ids[k] with the teacher's
+ *   logit top_logits[k] (domino_top_logits gives both).
+ *   teacher_lse NULL: p = softmax over the row's entries of top_logits / temperature, and
+ *     loss = w * sum_k p_k (log p_k - log q[id_k])
+ *   teacher_lse given (the teacher's log-sum-exp at this temperature): p_k = exp(top_logits[k] /
+ *     temperature - teacher_lse), and all other tokens form one class, of mass rho = max(0, 1 - sum p)
+ *     for the teacher and tau = sum of q over tokens that are no entry for the student:
+ *     loss = w * (sum_k p_k (log p_k - log q[id_k]) + rho (log rho - log tau))
+ *   Gradient, with P = sum p + rho:  w / temperature * (P q_v - p_v)               for an entry's token,
+ *                                    w / temperature * (P q_v - rho q_v / tau)     elsewhere.
+ * w = row_weights[row] (NULL: 1).  A row of weight 0 has loss 0 and gradient 0 and is not read.  So is
+ * a row without student mass, without an entry of positive mass (or with teacher_lse not finite): loss and
+ * gradient are 0.  Where the student has no mass outside the entries the term of the other tokens is
+ * left out.  A student that bars an entry of positive mass has loss +infinity.  Entries: id -1 is no
+ * entry (rows may have fewer than K); any other id outside [0, V) sets DOMINO_STATUS_BAD_TOKEN and is
+ * taken as none; a token given twice counts with both its masses, each a term of the sum.
+ *   top_ids [rows, K] int32, top_logits [rows, K] fp32, 1 <= K <= DOMINO_MAX_TOP; teacher_lse and
+ *   row_weights [rows] fp32 or NULL.
+ *
+ * domino_distill: loss [rows] fp32; stats [rows, 8] fp32 (16-byte aligned) for domino_distill_backward,
+ *   or NULL when grad is NULL too; grad, or NULL: the gradient of the sum of the rows' losses, rows of V
+ *   values grad_ld apart (a multiple of 8, >= V, 16-byte aligned base) in grad_dtype, rounded once;
+ *   columns from V on are left as they were.
+ * domino_distill_backward: the gradient of sum_r grad_loss[r] * loss[r] (grad_loss NULL: 1) from the
+ *   same arguments and the stats that domino_distill wrote for them; a row whose grad_loss is 0 is not
+ *   read and its gradient is 0.
+ * grad may be the logits themselves (same ld and dtype); no other overlap of outputs with inputs is
+ * allowed (DOMINO_ERR_INVALID_ARGUMENT). */
+typedef struct {
+  int32_t rows, V;
+  int64_t ld;
+  int32_t dtype, K;
+  const void* logits;
+  const int32_t* top_ids;
+  const float* top_logits;
+  const float* teacher_lse;
+  const float* row_weights;
+  float temperature;
+} domino_distill_t;
+
+DOMINO_API int domino_distill(const domino_distill_t* args, float* loss, float* stats, void* grad, int64_t grad_ld,
+                              int32_t grad_dtype, int32_t* status_dev, domino_stream_t stream);
+DOMINO_API int domino_distill_backward(const domino_distill_t* args, const float* stats, const float* grad_loss,
+                                       void* grad, int64_t grad_ld, int32_t grad_dtype, int32_t* status_dev,
+                                       domino_stream_t stream);
+
 /* Human-readable text for a DOMINO_ERR_* or DOMINO_STATUS_* code (static storage). */
 DOMINO_API const char* domino_status_string(int code);
 
