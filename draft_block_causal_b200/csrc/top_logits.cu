@@ -1,44 +1,52 @@
 // top_logits.cu -- the k largest logits of every row, in order, with the row's log-sum-exp.
 //
 // A row is read once, by a cluster of blocks that take contiguous slices of it.  A block walks its slice in
-// tiles of kVecs 16-byte vectors a thread, held in registers: each thread takes its tile maximum and adds the
-// tile's exponentials; then a threshold says which values can still be among the k largest, and those go to
-// a list in shared memory.  The threshold comes from the thread maxima alone: a value that k threads' maxima
-// reach has k values at or above it, so the k largest are at or above it too, and about as many values as
-// threads are (a thread's second largest rarely is).  It is found by bisection over the order-preserving bits
-// of the maxima, one __syncthreads_count a probe.  In later tiles, whose columns are higher, a value has to
-// exceed the threshold.  Should one tile still bring more values than the list holds (all large values in one
-// thread's columns, or a row of equal ones), the exact k are selected from the registers by bisection over
-// value and column.  Each block ranks its list; block 0 receives the blocks' sorted lists and sums through
-// distributed shared memory, and ranks a key by binary search in each.
+// tiles of kVecs 16-byte vectors a thread, the next tile's loads in flight while one is worked on: each thread
+// takes its vectors' maxima, adds the tile's exponentials, and puts the values that reach a bar, and so can
+// still be among the k largest, into a list in shared memory.  The bar comes from the threads' running maxima:
+// a value that k threads' maxima reach has k values at or above it, and not many more than k, as a thread's
+// second largest is rarely among them.  The least of the warps' j-th largest maxima, j = k / warps, is such a
+// value, and takes one barrier (an exact k-th by bisection, one barrier a probe, took four times as long).  It
+// is raised after 1, 3, 9, 27, ... tiles only, so that between them no thread waits for another; each such
+// stretch adds about 2k values.  A value in a later tile, whose column is higher, has to exceed the bar.
+// Should a stretch bring more than the list holds (ascending rows, many equal values), the exact k are selected
+// from the stretch, read again, and the list.  At the end the list is cut by the bar and goes to block 0, with
+// the sum, through distributed shared memory; block 0 cuts and ranks what it has got.
 #include "cluster.cuh"
 #include "launch.cuh"
 #include "vocab_rows.cuh"
 #include "vocab_rows.h"
 
+#include <cfloat>
+
 namespace domino {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 8;        // 16-byte vectors a thread and tile
-constexpr int kList = 2048;     // candidates held; a tile adds about k + k * k / 1024
-constexpr int kTidy = 1024;     // more than this are cut to the k largest before the next tile
+constexpr int kVecs = 4;        // 16-byte vectors a thread and tile
+constexpr int kList = 2048;     // candidates held
+constexpr int kTidy = 1024;     // a list longer than this is cut by the bar before the next stretch
 constexpr int kMaxCluster = 16;
-constexpr int kMaxK = DOMINO_MAX_TOP;
+
+// Keys a block of a cluster may hand to block 0: k or more, and kList of all blocks together.
+__host__ __device__ constexpr int share_of(int cluster) { return cluster > 8 ? 128 : 256; }
 
 struct TopShared {
   uint64_t list[kList];
-  uint64_t sorted[kMaxCluster][kMaxK];  // block 0: every block's k largest in order
-  double sum[kMaxCluster];              // block 0: every block's sum ...
-  float ref[kMaxCluster][2];            // ... its reference and maximum
+  double sum[kMaxCluster];    // block 0: every block's sum ...
+  float ref[kMaxCluster][2];  // ... its reference and maximum
   double red_s[kWarps];
   float red_n[kWarps], red_m[kWarps];
-  uint32_t red_u[2][kWarps];
+  uint32_t red_u[kWarps];
   int red_i[kWarps];
   int count;
+  int handed[kMaxCluster];    // block 0: keys of every block
 };
+
+// The least float of order o or more; the orders below -FLT_MAX's are no floats'.
+__device__ __forceinline__ float floor_at(uint32_t o) { return order_value(max(o, 0x00800000u)); }
 
 template <typename T> __device__ __forceinline__ uint4 barred_vec();
 template <> __device__ __forceinline__ uint4 barred_vec<float>() {
@@ -67,37 +75,37 @@ __device__ __forceinline__ float vec_max(const uint4& q, bf16) {
   return fmaxf(f.x, f.y);
 }
 
-// Adds a tile with maximum m > -infinity to the thread's sum; its first `vecs` vectors hold columns.
+// Adds a tile with maximum m > -infinity to the thread's sum.
 template <typename T>
-__device__ __forceinline__ void add_tile(ExpSum& a, const uint4 (&q)[kVecs], int vecs, float m, float c) {
+__device__ __forceinline__ void add_tile(ExpSum& a, const uint4 (&q)[kVecs], float m, float c) {
   const float n = fmaxf(a.n, reference_of(m, c));
   if (n > a.n) raise(a, n);
-  float s0 = 0.f, s1 = 0.f;
+  float2 s = make_float2(0.f, 0.f);
   if (!is_extreme(m)) {
+    const float2 c2 = make_float2(c, c), n2 = make_float2(-n, -n);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      if (i >= vecs) break;
       float z[Vec<T>::N];
       widen(q[i], z);
 #pragma unroll
       for (int e = 0; e < Vec<T>::N; e += 2) {
-        s0 += ex2(fmaf(z[e], c, -n));
-        s1 += ex2(fmaf(z[e + 1], c, -n));
+        const float2 x = fma2(make_float2(z[e], z[e + 1]), c2, n2);
+        s = add2(s, make_float2(ex2(x.x), ex2(x.y)));
       }
     }
   }
-  float s = s0 + s1;
-  if (is_extreme(m) || isnan(s)) {
-    s = 0.f;
+  float t = s.x + s.y;
+  if (is_extreme(m) || isnan(t)) {
+    t = 0.f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       float z[Vec<T>::N];
       widen(q[i], z);
 #pragma unroll
-      for (int e = 0; e < Vec<T>::N; ++e) s += term_guarded(z[e], c, n);
+      for (int e = 0; e < Vec<T>::N; ++e) t += term_guarded(z[e], c, n);
     }
   }
-  a.s += s;
+  a.s += t;
 }
 
 // Block 0's thread 0 gets sums over the block's threads.
@@ -130,62 +138,60 @@ __device__ __forceinline__ void join_threads(const ExpSum& a, float m, TopShared
   *max = mm;
 }
 
-// The list's keys in order, cut to k: sh.list[0 .. min(k, n)).  All threads call it; returns the new count.
-__device__ __forceinline__ int tidy(TopShared& sh, int n, int k, uint64_t* to) {
-  constexpr int kEach = kList / kThreads;
-  uint64_t key[kEach];
-  int rank[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int at = threadIdx.x + i * kThreads;
-    key[i] = 0;
-    rank[i] = 0;
-    if (at >= n) continue;
-    key[i] = sh.list[at];
-    for (int j = 0; j < n; ++j) rank[i] += sh.list[j] > key[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (key[i] != 0 && rank[i] < k) to[rank[i]] = key[i];
-  const int left = min(n, k);
-  if (threadIdx.x == 0) sh.count = left;
-  __syncthreads();
-  return left;
-}
+constexpr int kSlots = kList / kThreads;
 
-// A value that at least k of the threads' maxima reach, from their order bits `o` (at least k are not 0).
-__device__ __forceinline__ uint32_t reached_by(uint32_t o, int k, TopShared& sh) {
-  const uint32_t hi_w = __reduce_max_sync(0xffffffffu, o), lo_w = __reduce_min_sync(0xffffffffu, o);
-  if ((threadIdx.x & 31) == 0) {
-    sh.red_u[0][threadIdx.x >> 5] = lo_w;
-    sh.red_u[1][threadIdx.x >> 5] = hi_w;
-  }
-  __syncthreads();
-  uint32_t lo = sh.red_u[0][0], hi = sh.red_u[1][0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
-    lo = min(lo, sh.red_u[0][w]);
-    hi = max(hi, sh.red_u[1][w]);
-  }
-  lo = max(lo, 1u);
-  hi += 1;  // at least k reach lo, fewer than k reach hi
-  const int enough = k + k / 4 + 8;
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int c = __syncthreads_count(o >= mid);
-    if (c >= k) {
-      lo = mid;
-      if (c <= enough) break;
-    } else {
-      hi = mid;
+// An order that at least k of the threads' orders o (0: none) reach.  `warps`: the warps to look at, all of whose
+// lanes take part, warps * 32 >= k.  Where one has too few values the result is 0, which all reach.
+__device__ __forceinline__ uint32_t reached_by(uint32_t o, int warps, int k, TopShared& sh) {
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t top = 0xffffffffu;
+  if (wid < warps) {
+    top = __reduce_max_sync(0xffffffffu, o);
+    for (int j = (k + warps - 1) / warps; j > 1; --j) {
+      if (lane == __ffs(__ballot_sync(0xffffffffu, o == top)) - 1) o = 0;  // one lane takes it out
+      top = __reduce_max_sync(0xffffffffu, o);
     }
   }
-  return lo;
+  __syncthreads();  // an earlier result has been read
+  if (lane == 0) sh.red_u[wid] = top;
+  __syncthreads();
+  uint32_t r = sh.red_u[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) r = min(r, sh.red_u[w]);
+  return r;
 }
 
-// The least float above x < infinity.
-__device__ __forceinline__ float nextafter_up(float x) { return order_value(order_of(x) ? order_of(x) + 1 : 0x00800000u); }
+__device__ __forceinline__ uint32_t order_bits(uint64_t key) { return (uint32_t)(key >> 32); }
+
+// Cuts the list's n keys to those of order `bar` or more; returns how many.  Ends with a barrier.
+__device__ __forceinline__ int cut_list(TopShared& sh, int n, uint32_t bar) {
+  uint64_t key[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int at = threadIdx.x + i * kThreads;
+    key[i] = at < n ? sh.list[at] : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (key[i] != 0 && order_bits(key[i]) >= bar) sh.list[atomicAdd(&sh.count, 1)] = key[i];
+  __syncthreads();
+  return sh.count;
+}
+
+// f(key, rank) for each of n keys below rank k.
+template <typename F>
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, F f) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t own = keys[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += keys[j] > own;
+    if (rank < k) f(own, rank);
+  }
+}
 
 __device__ __forceinline__ int block_count(int n, TopShared& sh) {
   n = __reduce_add_sync(0xffffffffu, n);
@@ -199,13 +205,12 @@ __device__ __forceinline__ int block_count(int n, TopShared& sh) {
 }
 
 // The exact k of the `held` keys in the list and of the vectors [t0, t1) of a row, read again, into the list.
-// Returns the least value kept.
+// Returns the order of the least value kept.
 template <typename T>
-__device__ __noinline__ float select_exact(const T* row, int t0, int t1, int V, int held, int k, TopShared& sh) {
-  constexpr int kEach = kList / kThreads;
-  uint64_t own[kEach];
+__device__ __noinline__ uint32_t select_exact(const T* row, int t0, int t1, int V, int held, int k, TopShared& sh) {
+  uint64_t own[kSlots];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     const int at = threadIdx.x + i * kThreads;
     own[i] = at < held ? sh.list[at] : 0;
   }
@@ -216,7 +221,7 @@ __device__ __noinline__ float select_exact(const T* row, int t0, int t1, int V, 
         if (v + e < V) f(select_key(order_of(to_f32(row[v + e])), v + e));
     }
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) f(own[i]);
+    for (int i = 0; i < kSlots; ++i) f(own[i]);
   };
   uint64_t lo = 0;  // the largest key with at least k at or above it: keys are all different
   for (int bit = 63; bit >= 0; --bit) {
@@ -232,13 +237,14 @@ __device__ __noinline__ float select_exact(const T* row, int t0, int t1, int V, 
     if (key >= lo) sh.list[atomicAdd(&sh.count, 1)] = key;
   });
   __syncthreads();
-  return order_value((uint32_t)(lo >> 32));
+  return (uint32_t)(lo >> 32);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_top_rows(TopRows a, int cluster) {
+__global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster) {
   constexpr int N = Vec<T>::N;
   __shared__ TopShared sh;
+  extern __shared__ uint64_t handed[];  // block 0: [cluster][share_of(cluster)] keys
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x / cluster, tid = threadIdx.x;
@@ -249,122 +255,134 @@ __global__ void __launch_bounds__(kThreads, 2) k_top_rows(TopRows a, int cluster
   const T* row = static_cast<const T*>(a.logits) + (size_t)r * a.ld;
   const int all = (a.V + N - 1) / N, per = (all + cluster - 1) / cluster;
   const int first = min((int)rank * per, all), last = min(first + per, all);
-  ExpSum acc;
-  float m = -INFINITY, bar = -INFINITY;
-  int held = 0;  // keys in the list
-  for (int t0 = first; t0 < last; t0 += kThreads * kVecs) {
-    const int vecs = min((last - t0 + kThreads - 1) / kThreads, kVecs);  // vectors of the tile's first thread
-    uint4 q[kVecs];
+  constexpr int kTile = kThreads * kVecs;
+  auto load = [&](uint4(&q)[kVecs], int t0) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int vec = t0 + i * kThreads + tid;
       q[i] = vec < last ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
     }
-    if (a.V % N != 0 && t0 + kThreads * kVecs >= all) {
+    if (a.V % N != 0 && t0 + kTile >= all) {
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) q[i] = cut_vec<T>(q[i], (t0 + i * kThreads + tid) * N, a.V);
     }
-    float vm[kVecs], tm = -INFINITY;
+  };
+  const int warps = min(last - first, kThreads) / 32;  // warps with a vector in every lane
+  const bool can_bar = warps * 32 >= a.k;
+  ExpSum acc;
+  float m = -INFINITY;
+  uint32_t bar = 0;        // an order that k values so far reach
+  float floor = -FLT_MAX;  // values from here on go to the list
+  uint4 next[kVecs];
+  load(next, first);
+  int held = 0, before = 0, from = first, stop = first + kTile, stretch = 2 * kTile;
+  for (int t0 = first; t0 < last;) {
+    for (; t0 < min(stop, last); t0 += kTile) {
+      uint4 q[kVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      vm[i] = -INFINITY;
-      if (i < vecs) vm[i] = fmaxf(vec_max(q[i], T()), -INFINITY);
-      tm = fmaxf(tm, vm[i]);
-    }
-    if (tm > -INFINITY) {
-      m = fmaxf(m, tm);
-      add_tile<T>(acc, q, vecs, tm, a.c);
-    }
-    // the barrier also ends the previous tile's use of the list
-    const int hot = __syncthreads_count(tm > bar);
-    if (hot == 0) continue;
-    bool equal_too = false;  // the bar is this tile's own
-    if (hot >= a.k) {
-      const float own = order_value(reached_by(order_of(tm), a.k, sh));
-      equal_too = own > bar;
-      bar = fmaxf(bar, own);
-    }
-    const float floor = equal_too ? bar : nextafter_up(bar);  // values from here on go to the list
-    if (tm >= floor) {
+      for (int i = 0; i < kVecs; ++i) q[i] = next[i];
+      load(next, t0 + kTile);
+      float vm[kVecs], tm = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        if (vm[i] >= floor) {
-          const int v = (t0 + i * kThreads + tid) * N;
-          float z[N];
-          widen(q[i], z);
+        vm[i] = fmaxf(vec_max(q[i], T()), -INFINITY);
+        tm = fmaxf(tm, vm[i]);
+      }
+      if (tm > -INFINITY) {
+        m = fmaxf(m, tm);
+        add_tile<T>(acc, q, tm, a.c);
+      }
+      if (bar == 0 && can_bar) {  // no bar yet: this tile's columns may be the lowest that reach it
+        bar = reached_by(order_of(m), warps, a.k, sh);
+        floor = floor_at(bar);
+      }
+      if (tm >= floor) {
 #pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (z[e] >= floor) {
-              const int at = atomicAdd(&sh.count, 1);
-              if (at < kList) sh.list[at] = select_key(order_of(z[e]), v + e);
-            }
+        for (int i = 0; i < kVecs; ++i) {
+          if (vm[i] >= floor) {
+            const int v = (t0 + i * kThreads + tid) * N;
+            float z[N];
+            widen(q[i], z);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (z[e] >= floor) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kList) sh.list[at] = select_key(order_of(z[e]), v + e);
+              }
+          }
         }
       }
     }
     __syncthreads();
-    const int n = sh.count;
-    if (n > kList) {
-      bar = select_exact(row, t0, min(t0 + kThreads * kVecs, last), a.V, held, a.k, sh);
+    held = sh.count;
+    if (held > kList) {
+      bar = max(bar, select_exact(row, from, min(t0, last), a.V, before, a.k, sh));
       held = a.k;
-    } else if (n > kTidy && t0 + kThreads * kVecs < last) {
-      held = tidy(sh, n, a.k, sh.list);
-      bar = fmaxf(bar, order_value((uint32_t)(sh.list[a.k - 1] >> 32)));
-    } else {
-      held = n;
+    } else if (can_bar) {
+      bar = max(bar, reached_by(order_of(m), warps, a.k, sh));
     }
+    if (held > kTidy) held = cut_list(sh, held, bar);
+    if (bar) floor = floor_at(bar + 1);
+    before = held;
+    from = t0;
+    stop = t0 + stretch;
+    stretch *= 3;
+    __syncthreads();  // every thread has read the count before the next values come
   }
-  __syncthreads();
-  const int found = tidy(sh, held, a.k, sh.sorted[0]);
   double sum = 0.0;
   float ref = -INFINITY, max = -INFINITY;
   join_threads(acc, m, sh, &sum, &ref, &max);
-  float* const values = a.values + (size_t)r * a.k;
-  int32_t* const ids = a.ids + (size_t)r * a.k;
-  int have = found;
+  held = cut_list(sh, held, bar);
+  const uint64_t* keys = sh.list;
   if (cluster > 1) {
+    const int share = share_of(cluster);
+    if (held > share) {  // many equal values at the bar: the k largest alone
+      uint64_t own[kSlots];
+      int at[kSlots];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) at[i] = kList;
+      int i = 0;
+      rank_keys(sh.list, held, a.k, [&](uint64_t key, int rk) {
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (j == i) { own[j] = key; at[j] = rk; }
+        ++i;
+      });
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (at[j] < kList) sh.list[at[j]] = own[j];
+      held = a.k;
+      __syncthreads();
+    }
     cluster_wait();
-    if (rank != 0) {
-      const uint32_t to = cluster_address(sh.sorted[rank], 0);
-      for (int i = tid; i < a.k; i += kThreads) cluster_store(to + 8 * i, i < found ? sh.sorted[0][i] : (uint64_t)0);
-      if (tid == 0) {
-        cluster_store(cluster_address(&sh.sum[rank], 0), sum);
-        cluster_store(cluster_address(sh.ref[rank], 0), ref, max);
-      }
-    } else {
-      for (int i = found + tid; i < a.k; i += kThreads) sh.sorted[0][i] = 0;
-      if (tid == 0) {
-        sh.sum[0] = sum;
-        sh.ref[0][0] = ref;
-        sh.ref[0][1] = max;
-      }
+    const uint32_t to = cluster_address(handed + rank * share, 0);
+    for (int i = tid; i < held; i += kThreads) cluster_store(to + 8 * i, sh.list[i]);
+    if (tid == 0) {
+      cluster_store(cluster_address(&sh.sum[rank], 0), sum);
+      cluster_store(cluster_address(&sh.ref[rank], 0), ref, max);
+      cluster_store(cluster_address(&sh.handed[rank], 0), held);
     }
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;
-    have = 0;
-    const int total = cluster * a.k;
-    for (int i0 = 0; i0 < total; i0 += kThreads) {
-      const int i = i0 + tid, c = i / a.k, p = i % a.k;
-      const uint64_t key = i < total ? sh.sorted[c][p] : 0;
-      if (key != 0) {
-        int place = p;
-        for (int o = 0; o < cluster && place < a.k; ++o) {
-          if (o == c) continue;
-          int lo = 0, hi = a.k;  // keys before lo are larger, from hi on are not
-          while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (sh.sorted[o][mid] > key) lo = mid + 1;
-            else hi = mid;
-          }
-          place += lo;
-        }
-        if (place < a.k) {
-          values[place] = order_value((uint32_t)(key >> 32));
-          ids[place] = key_index(key);
-        }
+    // block 0: every block's keys, cut by a bar over them all, into its list again
+    const int places = cluster * share;
+    uint32_t o = 0;
+    held = 0;
+    for (int c = 0; c < cluster; ++c) held += sh.handed[c];
+    for (int i = tid; i < places; i += kThreads)
+      if (i % share < sh.handed[i / share]) o = umax(o, order_bits(handed[i]));
+    bar = held > kThreads ? reached_by(o, kWarps, a.k, sh) : 0;
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    for (int i = tid; i < places; i += kThreads)
+      if (i % share < sh.handed[i / share] && order_bits(handed[i]) >= bar) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kList) sh.list[at] = handed[i];
       }
-      have += __syncthreads_count(key != 0);
-    }
+    __syncthreads();
+    held = sh.count;
     if (tid == 0) {
       for (int c = 1; c < cluster; ++c) {
         ref = fmaxf(ref, sh.ref[c][0]);
@@ -374,14 +392,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_top_rows(TopRows a, int cluster
       for (int c = 0; c < cluster; ++c)
         if (sh.ref[c][0] > -INFINITY) sum += sh.sum[c] * (double)ex2(sh.ref[c][0] - ref);
     }
-  } else {
-    for (int i = tid; i < found; i += kThreads) {
-      const uint64_t key = sh.sorted[0][i];
-      values[i] = order_value((uint32_t)(key >> 32));
-      ids[i] = key_index(key);
-    }
   }
-  for (int i = have + tid; i < a.k; i += kThreads) {
+  float* const values = a.values + (size_t)r * a.k;
+  int32_t* const ids = a.ids + (size_t)r * a.k;
+  rank_keys(keys, held, a.k, [&](uint64_t key, int rk) {
+    values[rk] = order_value(order_bits(key));
+    ids[rk] = key_index(key);
+  });
+  for (int i = held + tid; i < a.k; i += kThreads) {
     values[i] = -INFINITY;
     ids[i] = -1;
   }
@@ -397,12 +415,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_top_rows(TopRows a, int cluster
 cudaError_t launch_top_rows(const TopRows& a, cudaStream_t st) {
   const bool f = a.dtype == DOMINO_DTYPE_F32;
   const int vecs = (a.V + (f ? 3 : 7)) / (f ? 4 : 8);
-  // enough blocks for two on each of 148 SMs, none with less than a vector a thread
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)a.rows * cluster < 4 * 296 && vecs / (2 * cluster) >= kThreads) cluster *= 2;
+  while (cluster < kMaxCluster && (int64_t)a.rows * cluster < 4 * 148 && vecs / (2 * cluster) >= 2 * kThreads) cluster *= 2;
   const dim3 grid((unsigned)a.rows * (unsigned)cluster);
-  return note_launch(f ? launch_cluster(k_top_rows<float>, cluster, grid, dim3(kThreads), 0, st, a, cluster)
-                       : launch_cluster(k_top_rows<bf16>, cluster, grid, dim3(kThreads), 0, st, a, cluster));
+  const size_t smem = cluster > 1 ? (size_t)cluster * share_of(cluster) * sizeof(uint64_t) : 0;
+  return note_launch(f ? launch_cluster(k_top_rows<float>, cluster, grid, dim3(kThreads), smem, st, a, cluster)
+                       : launch_cluster(k_top_rows<bf16>, cluster, grid, dim3(kThreads), smem, st, a, cluster));
 }
 
 }  // namespace domino
