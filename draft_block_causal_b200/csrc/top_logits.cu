@@ -31,10 +31,10 @@ constexpr int kTidy = 1024;     // a list longer than this is cut by the bar bef
 constexpr int kMaxCluster = 16;
 
 // Keys a block of a cluster may hand to block 0: k or more, and kList of all blocks together.
-__host__ __device__ constexpr int share_of(int cluster) { return cluster > 8 ? 128 : 256; }
+__host__ __device__ constexpr int share_bits(int cluster) { return cluster > 8 ? 7 : 8; }
 
 struct TopShared {
-  uint64_t list[kList];
+  alignas(16) uint64_t list[kList + 1];
   double sum[kMaxCluster];    // block 0: every block's sum ...
   float ref[kMaxCluster][2];  // ... its reference and maximum
   double red_s[kWarps];
@@ -43,6 +43,7 @@ struct TopShared {
   int red_i[kWarps];
   int count;
   int handed[kMaxCluster];    // block 0: keys of every block
+  uint32_t bars[kMaxCluster]; // block 0: every block's bar
 };
 
 // The least float of order o or more; the orders below -FLT_MAX's are no floats'.
@@ -181,14 +182,19 @@ __device__ __forceinline__ int cut_list(TopShared& sh, int n, uint32_t bar) {
   return sh.count;
 }
 
-// f(key, rank) for each of n keys below rank k.
+// f(key, rank) for each of the list's n keys below rank k.
 template <typename F>
-__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, F f) {
+__device__ __forceinline__ void rank_list(TopShared& sh, int n, int k, F f) {
+  if (threadIdx.x == 0) sh.list[n] = 0;  // pairs of keys are read at once
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t own = keys[i];
+    const uint64_t own = sh.list[i];
     int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) rank += keys[j] > own;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(sh.list + j);
+      rank += (two.x > own) + (two.y > own);
+    }
     if (rank < k) f(own, rank);
   }
 }
@@ -244,7 +250,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster) {
   constexpr int N = Vec<T>::N;
   __shared__ TopShared sh;
-  extern __shared__ uint64_t handed[];  // block 0: [cluster][share_of(cluster)] keys
+  extern __shared__ uint64_t handed[];  // block 0: [cluster][1 << share_bits(cluster)] keys
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x / cluster, tid = threadIdx.x;
@@ -330,19 +336,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
     __syncthreads();  // every thread has read the count before the next values come
   }
   double sum = 0.0;
-  float ref = -INFINITY, max = -INFINITY;
-  join_threads(acc, m, sh, &sum, &ref, &max);
+  float ref = -INFINITY, most = -INFINITY;
+  join_threads(acc, m, sh, &sum, &ref, &most);
   held = cut_list(sh, held, bar);
-  const uint64_t* keys = sh.list;
   if (cluster > 1) {
-    const int share = share_of(cluster);
+    const int bits = share_bits(cluster), share = 1 << bits;
     if (held > share) {  // many equal values at the bar: the k largest alone
       uint64_t own[kSlots];
       int at[kSlots];
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) at[i] = kList;
       int i = 0;
-      rank_keys(sh.list, held, a.k, [&](uint64_t key, int rk) {
+      rank_list(sh, held, a.k, [&](uint64_t key, int rk) {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
           if (j == i) { own[j] = key; at[j] = rk; }
@@ -360,33 +365,26 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
     for (int i = tid; i < held; i += kThreads) cluster_store(to + 8 * i, sh.list[i]);
     if (tid == 0) {
       cluster_store(cluster_address(&sh.sum[rank], 0), sum);
-      cluster_store(cluster_address(&sh.ref[rank], 0), ref, max);
+      cluster_store(cluster_address(&sh.ref[rank], 0), ref, most);
       cluster_store(cluster_address(&sh.handed[rank], 0), held);
+      cluster_store(cluster_address(&sh.bars[rank], 0), (int)bar);
     }
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;
-    // block 0: every block's keys, cut by a bar over them all, into its list again
-    const int places = cluster * share;
-    uint32_t o = 0;
-    held = 0;
-    for (int c = 0; c < cluster; ++c) held += sh.handed[c];
-    for (int i = tid; i < places; i += kThreads)
-      if (i % share < sh.handed[i / share]) o = umax(o, order_bits(handed[i]));
-    bar = held > kThreads ? reached_by(o, kWarps, a.k, sh) : 0;
+    // block 0: every block's keys that reach the highest of the blocks' bars, into its list
     if (tid == 0) sh.count = 0;
+    bar = 0;
+    for (int c = 0; c < cluster; ++c) bar = max(bar, sh.bars[c]);
     __syncthreads();
-    for (int i = tid; i < places; i += kThreads)
-      if (i % share < sh.handed[i / share] && order_bits(handed[i]) >= bar) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kList) sh.list[at] = handed[i];
-      }
+    for (int i = tid; i < cluster * share; i += kThreads)
+      if ((i & (share - 1)) < sh.handed[i >> bits] && order_bits(handed[i]) >= bar) sh.list[atomicAdd(&sh.count, 1)] = handed[i];
     __syncthreads();
     held = sh.count;
     if (tid == 0) {
       for (int c = 1; c < cluster; ++c) {
         ref = fmaxf(ref, sh.ref[c][0]);
-        max = fmaxf(max, sh.ref[c][1]);
+        most = fmaxf(most, sh.ref[c][1]);
       }
       sum = 0.0;
       for (int c = 0; c < cluster; ++c)
@@ -395,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
   }
   float* const values = a.values + (size_t)r * a.k;
   int32_t* const ids = a.ids + (size_t)r * a.k;
-  rank_keys(keys, held, a.k, [&](uint64_t key, int rk) {
+  rank_list(sh, held, a.k, [&](uint64_t key, int rk) {
     values[rk] = order_value(order_bits(key));
     ids[rk] = key_index(key);
   });
@@ -404,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
     ids[i] = -1;
   }
   if (tid == 0) {
-    const double lse = log_sum_exp(sum, ref, max, a.c, a.inv_t);
+    const double lse = log_sum_exp(sum, ref, most, a.c, a.inv_t);
     if (a.lse) a.lse[r] = (float)lse;
     if (a.lse64) a.lse64[r] = lse;
   }
@@ -418,7 +416,7 @@ cudaError_t launch_top_rows(const TopRows& a, cudaStream_t st) {
   int cluster = 1;
   while (cluster < kMaxCluster && (int64_t)a.rows * cluster < 4 * 148 && vecs / (2 * cluster) >= 2 * kThreads) cluster *= 2;
   const dim3 grid((unsigned)a.rows * (unsigned)cluster);
-  const size_t smem = cluster > 1 ? (size_t)cluster * share_of(cluster) * sizeof(uint64_t) : 0;
+  const size_t smem = cluster > 1 ? ((size_t)cluster << share_bits(cluster)) * sizeof(uint64_t) : 0;
   return note_launch(f ? launch_cluster(k_top_rows<float>, cluster, grid, dim3(kThreads), smem, st, a, cluster)
                        : launch_cluster(k_top_rows<bf16>, cluster, grid, dim3(kThreads), smem, st, a, cluster));
 }

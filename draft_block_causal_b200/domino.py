@@ -10,7 +10,6 @@ Names follow the C ABI without the ``domino_`` prefix: ``draft_greedy``, ``teach
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -602,10 +601,13 @@ def _logit_rows(t, name: str):
     code = _DTYPE_CODE.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} has dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
     if len(shape) < 2 or 0 in shape:
         raise ValueError(f"{name} must be a [..., V] tensor with at least one row, not {tuple(shape)}")
     V = shape[-1]
+    if V % 8 == 0 and t.is_contiguous():
+        return shape[:-1], V, V, code
+    strides = t.stride()
     ld = run = None
     for n, s in zip(shape[-2::-1], strides[-2::-1]):
         if n == 1:
@@ -628,16 +630,34 @@ def _logit_rows(t, name: str):
     return shape[:-1], V, ld, code
 
 
-def _empty_rows(lead, V: int, dtype, device):
+def _new(dims, dtype, device, stream):
+    """An uninitialised tensor whose memory belongs to the stream that the call uses it on."""
+    if stream is None:
+        return torch.empty(dims, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(dims, dtype=dtype, device=device)
+
+
+def _new_rows(lead, V: int, dtype, device, stream):
     """An uninitialised [..., V] tensor in rows padded to a multiple of 8 values."""
-    padded = (V + 7) // 8 * 8
-    t = torch.empty(tuple(lead) + (padded,), dtype=dtype, device=device)
-    return t if padded == V else t[..., :V]
+    if V % 8 == 0:
+        return _new(lead + (V,), dtype, device, stream)
+    return _new(lead + ((V + 7) // 8 * 8,), dtype, device, stream)[..., :V]
 
 
-def _allocating_on(stream):
-    """Memory that a call allocates belongs to the stream it is used on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _raw_stream(stream, device) -> int:
+    """``_stream`` as a plain handle, without the stream object of the current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"the call's tensors must be on a CUDA device, not {device}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors on {device}")
+    return stream.cuda_stream
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
 
 
 def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_out=None, lse_out=None, stream=None):
@@ -648,17 +668,19 @@ def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_ou
     dev, k = logits.device, int(k)
     if not 1 <= k <= MAX_TOP:
         raise ValueError(f"k is {k}, expected 1 to {MAX_TOP}")
-    sp = _stream(stream, dev)
-    with _allocating_on(stream):
-        if values_out is None:
-            values_out = torch.empty(lead + (k,), dtype=torch.float32, device=dev)
-        if ids_out is None:
-            ids_out = torch.empty(lead + (k,), dtype=torch.int32, device=dev)
-        if lse_out is None:
-            lse_out = torch.empty(lead, dtype=torch.float32, device=dev)
-    _expect(values_out, "values_out", lead + (k,), torch.float32, dev)
-    _expect(ids_out, "ids_out", lead + (k,), torch.int32, dev)
-    _expect(lse_out, "lse_out", lead, torch.float32, dev)
+    sp = _raw_stream(stream, dev)
+    if values_out is None:
+        values_out = _new(lead + (k,), torch.float32, dev, stream)
+    else:
+        _expect(values_out, "values_out", lead + (k,), torch.float32, dev)
+    if ids_out is None:
+        ids_out = _new(lead + (k,), torch.int32, dev, stream)
+    else:
+        _expect(ids_out, "ids_out", lead + (k,), torch.int32, dev)
+    if lse_out is None:
+        lse_out = _new(lead, torch.float32, dev, stream)
+    else:
+        _expect(lse_out, "lse_out", lead, torch.float32, dev)
     rc = _launch(dev, lib().domino_top_logits, logits.numel() // V, V, ld, code, logits.data_ptr(), k,
                  float(temperature), values_out.data_ptr(), ids_out.data_ptr(), lse_out.data_ptr(), sp)
     _check(rc, "domino_top_logits")
@@ -708,38 +730,36 @@ def beam_select(logits, scores, beams: int, states=None, history=None, pos: int 
         _expect(history, "history", (B, W, hist_len), torch.int32, dev)
     if finished is not None:
         _expect(finished, "finished", (B, W), torch.uint8, dev)
-    sp = _stream(stream, dev)
-    with _allocating_on(stream):
-        if out is None:
-            out = BeamStep(torch.empty((B, n), dtype=torch.float32, device=dev),
-                           torch.empty((B, n), dtype=torch.int32, device=dev),
-                           torch.empty((B, n), dtype=torch.int32, device=dev),
-                           None if states is None else torch.empty((B, n, Hs), dtype=torch.float32, device=dev),
-                           None if history is None else torch.empty((B, n, hist_len), dtype=torch.int32, device=dev),
-                           None if eos < 0 else torch.empty((B, n), dtype=torch.uint8, device=dev))
-        else:
-            _expect(out.scores, "out.scores", (B, n), torch.float32, dev)
-            _expect(out.parents, "out.parents", (B, n), torch.int32, dev)
-            _expect(out.tokens, "out.tokens", (B, n), torch.int32, dev)
-            for name, given, dims, dt in (("states", states, (B, n, Hs), torch.float32),
-                                          ("history", history, (B, n, hist_len), torch.int32)):
-                t = getattr(out, name)
-                if (t is None) != (given is None):
-                    raise ValueError(f"out.{name} must be given exactly when {name} is")
-                if t is not None:
-                    _expect(t, f"out.{name}", dims, dt, dev)
-            if out.finished is not None:
-                _expect(out.finished, "out.finished", (B, n), torch.uint8, dev)
-        if workspace is None:
-            nbytes = beam_workspace_bytes(B, W, n)
-            if nbytes == 0:
-                raise DominoError(ERR_UNSUPPORTED, "domino_beam_workspace_bytes")
-            workspace = alloc_workspace(nbytes, dev)
-    _expect_workspace(workspace, dev)
-    ptr = lambda t: None if t is None else t.data_ptr()
+    sp = _raw_stream(stream, dev)
+    if out is None:
+        three = _new((3, B, n), torch.int32, dev, stream).unbind(0)
+        out = BeamStep(three[0].view(torch.float32), three[1], three[2],
+                       None if states is None else _new((B, n, Hs), torch.float32, dev, stream),
+                       None if history is None else _new((B, n, hist_len), torch.int32, dev, stream),
+                       None if eos < 0 else _new((B, n), torch.uint8, dev, stream))
+    else:
+        _expect(out.scores, "out.scores", (B, n), torch.float32, dev)
+        _expect(out.parents, "out.parents", (B, n), torch.int32, dev)
+        _expect(out.tokens, "out.tokens", (B, n), torch.int32, dev)
+        for name, given, dims, dt in (("states", states, (B, n, Hs), torch.float32),
+                                      ("history", history, (B, n, hist_len), torch.int32)):
+            t = getattr(out, name)
+            if (t is None) != (given is None):
+                raise ValueError(f"out.{name} must be given exactly when {name} is")
+            if t is not None:
+                _expect(t, f"out.{name}", dims, dt, dev)
+        if out.finished is not None:
+            _expect(out.finished, "out.finished", (B, n), torch.uint8, dev)
+    if workspace is None:
+        nbytes = beam_workspace_bytes(B, W, n)
+        if nbytes == 0:
+            raise DominoError(ERR_UNSUPPORTED, "domino_beam_workspace_bytes")
+        workspace = _new((nbytes,), torch.uint8, dev, stream)
+    else:
+        _expect_workspace(workspace, dev)
     a = BeamArgs(B, W, n, V, ld, code, int(eos), Hs, hist_len, int(pos), logits.data_ptr(), scores.data_ptr(),
-                 ptr(finished), ptr(states), ptr(history), out.scores.data_ptr(), out.parents.data_ptr(),
-                 out.tokens.data_ptr(), ptr(out.finished), ptr(out.states), ptr(out.history))
+                 _data(finished), _data(states), _data(history), out.scores.data_ptr(), out.parents.data_ptr(),
+                 out.tokens.data_ptr(), _data(out.finished), _data(out.states), _data(out.history))
     rc = _launch(dev, lib().domino_beam_select, ctypes.byref(a), workspace.data_ptr(), workspace.numel(), sp)
     _check(rc, "domino_beam_select")
     return out
@@ -760,9 +780,8 @@ def _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_wei
         _expect(teacher_lse, "teacher_lse", lead, torch.float32, dev)
     if row_weights is not None:
         _expect(row_weights, "row_weights", lead, torch.float32, dev)
-    ptr = lambda t: None if t is None else t.data_ptr()
     return DistillArgs(logits.numel() // V, V, ld, code, K, logits.data_ptr(), top_ids.data_ptr(),
-                       top_logits.data_ptr(), ptr(teacher_lse), ptr(row_weights), float(temperature)), lead, V
+                       top_logits.data_ptr(), _data(teacher_lse), _data(row_weights), float(temperature)), lead, V
 
 
 def _expect_grad(grad, lead, V, dev):
@@ -788,25 +807,25 @@ def distill(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 
     ``distill_backward``."""
     a, lead, V = _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_weights)
     dev = logits.device
-    sp = _stream(stream, dev)
-    with _allocating_on(stream):
-        if loss_out is None:
-            loss_out = torch.empty(lead, dtype=torch.float32, device=dev)
-        if stats_out is None:
-            stats_out = torch.empty(lead + (8,), dtype=torch.float32, device=dev)
-        if grad_out is True:
-            grad_out = _empty_rows(lead, V, logits.dtype, dev)
+    sp = _raw_stream(stream, dev)
+    if loss_out is None:
+        loss_out = _new(lead, torch.float32, dev, stream)
+    else:
+        _expect(loss_out, "loss_out", lead, torch.float32, dev)
+    if stats_out is None:
+        stats_out = _new(lead + (8,), torch.float32, dev, stream)
+    else:
+        _expect(stats_out, "stats_out", lead + (8,), torch.float32, dev)
+    _expect_status(status, dev)
     if grad_out is False:
         grad_out = None
-    _expect(loss_out, "loss_out", lead, torch.float32, dev)
-    _expect(stats_out, "stats_out", lead + (8,), torch.float32, dev)
-    _expect_status(status, dev)
-    gptr, gld, gcode = None, 0, 0
+    gld = gcode = 0
     if grad_out is not None:
+        if grad_out is True:
+            grad_out = _new_rows(lead, V, logits.dtype, dev, stream)
         gld, gcode = _expect_grad(grad_out, lead, V, dev)
-        gptr = grad_out.data_ptr()
-    rc = _launch(dev, lib().domino_distill, ctypes.byref(a), loss_out.data_ptr(), stats_out.data_ptr(), gptr, gld,
-                 gcode, _ptr(status), sp)
+    rc = _launch(dev, lib().domino_distill, ctypes.byref(a), loss_out.data_ptr(), stats_out.data_ptr(),
+                 _data(grad_out), gld, gcode, _data(status), sp)
     _check(rc, "domino_distill")
     return loss_out, grad_out, stats_out
 
@@ -820,14 +839,13 @@ def distill_backward(logits, top_ids, top_logits, stats, grad_loss=None, teacher
     _expect(stats, "stats", lead + (8,), torch.float32, dev)
     if grad_loss is not None:
         _expect(grad_loss, "grad_loss", lead, torch.float32, dev)
-    sp = _stream(stream, dev)
+    sp = _raw_stream(stream, dev)
     if grad_out is None or grad_out is True:
-        with _allocating_on(stream):
-            grad_out = _empty_rows(lead, V, logits.dtype, dev)
+        grad_out = _new_rows(lead, V, logits.dtype, dev, stream)
     gld, gcode = _expect_grad(grad_out, lead, V, dev)
     _expect_status(status, dev)
-    rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(),
-                 None if grad_loss is None else grad_loss.data_ptr(), grad_out.data_ptr(), gld, gcode, _ptr(status), sp)
+    rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(), _data(grad_loss),
+                 grad_out.data_ptr(), gld, gcode, _data(status), sp)
     _check(rc, "domino_distill_backward")
     return grad_out
 
