@@ -49,13 +49,6 @@ struct TopShared {
 // The least float of order o or more; the orders below -FLT_MAX's are no floats'.
 __device__ __forceinline__ float floor_at(uint32_t o) { return order_value(max(o, 0x00800000u)); }
 
-template <typename T> __device__ __forceinline__ uint4 barred_vec();
-template <> __device__ __forceinline__ uint4 barred_vec<float>() {
-  return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-}
-template <> __device__ __forceinline__ uint4 barred_vec<bf16>() {
-  return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-}
 // The vector at column v of a row of V with the columns from V on barred.
 template <typename T>
 __device__ __forceinline__ uint4 cut_vec(uint4 q, int v, int V) {
@@ -64,16 +57,6 @@ __device__ __forceinline__ uint4 cut_vec(uint4 q, int v, int V) {
   for (int i = 0; i < Vec<T>::N; ++i)
     if (v + i >= V) e[i] = static_cast<T>(-INFINITY);
   return q;
-}
-
-// The largest value of a vector (NaN aside); bf16 pairs go through one packed maximum.
-__device__ __forceinline__ float vec_max(const uint4& q, float) {
-  return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
-}
-__device__ __forceinline__ float vec_max(const uint4& q, bf16) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-  const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-  return fmaxf(f.x, f.y);
 }
 
 // Adds a tile with maximum m > -infinity to the thread's sum.

@@ -42,7 +42,10 @@ def test_distillation_step_of_the_head(logits_dtype):
     loss.sum().backward()
     fused, grad, _ = domino.distill(z, ids, top, lse, T, weights, grad_out=True)
     torch.cuda.synchronize()
-    assert torch.equal(fused, loss.detach())
+    # the loss alone and the loss with its gradient add a row's terms in different orders, each within
+    # 4 SUM(V) + 2^-23 |loss| of the definition: they differ by at most twice that
+    near = 2 * (4 * R.sum_tol(V) + 2.0 ** -23 * loss.detach().abs())
+    assert ((fused - loss.detach()).abs() <= near).all()
     # the operators on the head's own logits
     zz = logits.detach().double().cpu().numpy().reshape(-1, V)
     args = (ids.cpu().numpy().reshape(-1, K), top.double().cpu().numpy().reshape(-1, K),
