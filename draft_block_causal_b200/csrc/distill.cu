@@ -8,15 +8,16 @@
 // are added in 64 bits: S_rest as S less the entries' terms would be lost for a student that puts all but 1e-7 of
 // its mass on them.  log p_k is y_k less the entries' log-sum, so the entries need one exponential each.
 //
-// Loss and gradient in one call read a row once: a cluster of blocks holds it in registers (k_distill_row),
-// the blocks exchange their sums through distributed shared memory, and each writes its slice's gradient.
-// The entries take one warp of a block; block 0's also forms what the others need of them.  Rows that no
-// cluster holds, the loss alone and the backward call go by k_distill_sum (a row's sums by a cluster, read
-// once) and k_distill_grad (elementwise from the stats).
+// A cluster of blocks takes a row (k_distill): each sums its slice, they exchange sums through distributed shared
+// memory, and for the gradient each reads its slice again, out of L2, and writes.  A block deals with the entries
+// whose columns it has, in a warp of their own.  The backward call is elementwise from the stats (k_distill_grad).
 #include "cluster.cuh"
 #include "launch.cuh"
 #include "vocab_rows.cuh"
 #include "vocab_rows.h"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace domino {
 
@@ -24,6 +25,7 @@ namespace {
 
 constexpr int kMaxK = DOMINO_MAX_TOP;
 constexpr int kMaxCluster = 16;
+constexpr int kEach = kMaxK / 32;  // entries a lane of the entries' warp
 
 struct DistillArgs {
   domino_distill_t d;
@@ -55,33 +57,30 @@ __device__ __forceinline__ Stats load_stats(const float4* st, int r) {
   return Stats{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// Block 0's findings on a row's entries, for every block of the cluster.
-struct Top {
-  double sum, psum, lp;  // sum * 2^ref: the distinct entries' terms of S; sum of p; log-sum of the entries' y
-  double lead;           // sum of p (log p - x)
-  float ref;
-  int live, twice;       // whether the row counts; whether a token is given twice
-};
-// A block's sum over its columns that are no entry's.
-struct Part {
-  double s;
-  float n, m;
+// What a block of a cluster knows of a row: sums over its columns, references and maximum.
+struct Record {
+  double s;    // terms of the columns that are no entry's, times 2^-n
+  double ts;   // terms of its entries' distinct tokens, times 2^-tn
+  double z;    // sum of exp(y - my) over its entries
+  double a;    // sum of exp(y - my) (y - x)
+  float n, m, tn;
 };
 
-// A row's entries, in the hands of one warp: lane l has entries l, l + 32, ...
-struct Entries {
-  int32_t id[kMaxK];  // -1: none
-  double y[kMaxK];    // the teacher's logit over T, -infinity for one without mass
-  double x[kMaxK];    // the student's, where it was asked for
-  double p[kMaxK];
+// The entries of a row whose columns a block has.
+struct Own {
+  int n;             // how many
+  int live;          // the teacher's row counts
+  double my;         // what y is taken from: teacher_lse, or the row's largest y
+  int32_t id[kMaxK];
+  double y[kMaxK];
 };
 
-struct DistillShared {
-  Part parts[kMaxCluster];
-  Top top;
-  double red_s[32];
-  float red_n[32], red_m[32];
-  Entries en;
+// What one warp makes of them.
+struct OwnSums {
+  float e[kMaxK];    // 2^(log2(e) x - tn)
+  float p[kMaxK];    // exp(y - my), all of the token's entries at its first, -1 at the others
+  float tn;
+  double ts, z, a;   // as in Record
 };
 
 __device__ __forceinline__ double warp_add(double v) {
@@ -89,88 +88,119 @@ __device__ __forceinline__ double warp_add(double v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-// Reads a row's entries; x for those with columns in [v0, v1).  One warp; ends with its barrier.
-template <typename T>
-__device__ __forceinline__ void load_entries(const DistillArgs& a, int r, const T* row, int v0, int v1, Entries& en,
-                                             bool report) {
+// One warp: a row's entries, one k = 32 i + lane after the other, for the block with columns [v0, v1).  Ends with the
+// warp's barrier.
+__device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, int v1, Own& own, bool report) {
   const domino_distill_t& d = a.d;
-  for (int k = threadIdx.x & 31; k < d.K; k += 32) {
-    int id = __ldg(d.top_ids + (size_t)r * d.K + k);
-    const float t = __ldg(d.top_logits + (size_t)r * d.K + k);
-    if (id < 0 || id >= d.V) {
-      if (id != -1 && report && a.status) set_status(a.status, DOMINO_STATUS_BAD_TOKEN);
-      id = -1;
+  const int lane = threadIdx.x & 31;
+  int32_t id[kEach];
+  float t[kEach], most = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = 32 * i + lane;
+    id[i] = -1;
+    t[i] = -INFINITY;
+    if (k < d.K) {
+      id[i] = __ldg(d.top_ids + (size_t)r * d.K + k);
+      t[i] = __ldg(d.top_logits + (size_t)r * d.K + k);
     }
-    en.id[k] = id;
-    en.y[k] = id >= 0 && t > -INFINITY ? (double)big_clamp(t) * a.inv_t : -INFINITY;
-    double x = -INFINITY;
-    if (id >= v0 && id < v1) {
-      const float z = to_f32(row[id]);
-      if (z > -INFINITY) x = (double)big_clamp(z) * a.inv_t;
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (id[i] < 0 || id[i] >= d.V) {
+      if (id[i] != -1 && report && a.status) set_status(a.status, DOMINO_STATUS_BAD_TOKEN);
+      id[i] = -1;
+    } else {
+      most = fmaxf(most, t[i]);
     }
-    en.x[k] = x;
+    const bool mine = id[i] >= v0 && id[i] < v1;  // -1 is not
+    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+    if (mine) {
+      const int at = n + __popc(all & ((1u << lane) - 1));
+      own.id[at] = id[i];
+      own.y[at] = t[i] > -INFINITY ? (double)big_clamp(t[i]) * a.inv_t : -INFINITY;
+    }
+    n += __popc(all);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) {
+    own.n = n;
+    if (d.teacher_lse) {
+      const float lse = d.teacher_lse[r];
+      own.live = fabsf(lse) < INFINITY;
+      own.my = own.live ? (double)lse : 0.0;
+    } else {
+      own.live = most > -INFINITY;
+      own.my = own.live ? (double)big_clamp(most) * a.inv_t : 0.0;
+    }
   }
   __syncwarp();
 }
 
-// What block 0's entries' warp finds: sh.top.
-__device__ __forceinline__ void find_top(const DistillArgs& a, int r, DistillShared& sh) {
-  const domino_distill_t& d = a.d;
-  const Entries& en = sh.en;
-  const int lane = threadIdx.x & 31;
-  Top t{};
-  double m = -INFINITY, top = -INFINITY;
-  for (int k = lane; k < d.K; k += 32) {
-    m = fmax(m, en.y[k]);
-    top = fmax(top, en.x[k]);
-  }
-  if (d.teacher_lse) {
-    const float lse = d.teacher_lse[r];
-    t.lp = lse;
-    t.live = fabsf(lse) < INFINITY;
-  } else {
-    m = warp_max(m);
-    double s = 0.0;
-    for (int k = lane; k < d.K; k += 32)
-      if (en.y[k] > -INFINITY) s += exp(en.y[k] - m);
-    t.lp = m + log(warp_add(s));
-    t.live = m > -INFINITY;
-  }
-  top = warp_max(top);
-  const double ref = top > -INFINITY ? ceil(top * kLog2e) : 0.0;
-  t.ref = (float)ref;
-  bool twice = false;
-  if (t.live) {
-    for (int k = lane; k < d.K; k += 32) {
-      const int id = en.id[k];
-      if (id < 0) continue;
-      bool first = true;
-      for (int j = 0; j < k && first; ++j) first = en.id[j] != id;
-      twice |= !first;
-      if (first && en.x[k] > -INFINITY) t.sum += exp2(en.x[k] * kLog2e - ref);
-      if (en.y[k] > -INFINITY) {
-        const double p = exp(en.y[k] - t.lp);
-        t.psum += p;
-        if (p > 0.0) t.lead += p * (en.y[k] - t.lp - en.x[k]);
-      }
-    }
-  }
-  t.sum = warp_add(t.sum);
-  t.psum = warp_add(t.psum);
-  t.lead = warp_add(t.lead);
-  t.twice = __any_sync(0xffffffffu, twice);
-  if (!(t.psum > 0.0) && !isnan(t.psum)) t.live = 0;
-  if (lane == 0) sh.top = t;
-}
-
 // 2^(difference of references): no power of two that a term could see is left out.
 __device__ __forceinline__ double pow2(double e) { return e < -1000.0 ? 0.0 : e > 1000.0 ? INFINITY : ldexp(1.0, (int)e); }
+
+// 2^t of a number in 64 bits: its whole part is exact, the rest goes through the fp32 exponential, 2^-22.
+__device__ __forceinline__ double exp2_near(double t) {
+  const double n = rint(t);
+  return n < -1000.0 ? 0.0 : ldexp((double)ex2((float)(t - n)), (int)fmin(n, 1000.0));
+}
+
+// One warp: the sums over a block's entries, from their logits in `row`.
+template <typename T>
+__device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, const T* row, OwnSums& sums) {
+  const int lane = threadIdx.x & 31, n = own.n;
+  double ts = 0.0, zs = 0.0, as = 0.0;
+  float tn = -INFINITY;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const int k = k0 + lane;
+    const float z = k < n ? to_f32(row[own.id[k]]) : -INFINITY;
+    const double x = z > -INFINITY ? (double)big_clamp(z) * a.inv_t : -INFINITY;
+    float most = z > -INFINITY ? (float)ceil(x * kLog2e) : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (most > tn) {  // entries before these are taken to the new reference
+      if (tn > -INFINITY) {
+        const double by = pow2((double)tn - (double)most);
+        ts *= by;
+        for (int j = lane; j < k0; j += 32) sums.e[j] *= (float)by;
+      }
+      tn = most;
+    }
+    if (k >= n) continue;
+    const int id = own.id[k];
+    const double y = own.y[k], pt = y > -INFINITY ? exp2_near((y - own.my) * kLog2e) : 0.0;
+    double p = pt;
+    const double e = x > -INFINITY ? exp2_near(x * kLog2e - (double)tn) : 0.0;
+    bool first = true;
+    for (int j = 0; j < n; ++j)
+      if (own.id[j] == id && j != k) {  // rare: a token given twice
+        first &= j > k;
+        if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - own.my) * kLog2e);
+      }
+    sums.e[k] = (float)e;
+    sums.p[k] = first ? (float)p : -1.f;
+    if (first) ts += e;
+    zs += pt;
+    if (pt > 0.0) as += pt * (y - x);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ts += __shfl_xor_sync(0xffffffffu, ts, o);
+    zs += __shfl_xor_sync(0xffffffffu, zs, o);
+    as += __shfl_xor_sync(0xffffffffu, as, o);
+  }
+  if (lane == 0) {
+    sums.tn = tn;
+    sums.ts = ts;
+    sums.z = zs;
+    sums.a = as;
+  }
+  __syncwarp();
+}
 
 // True S over the sum taken with c rounded to fp32: 2^(delta m).
 __device__ __forceinline__ double rounding_of_c(float m, float c, double inv_t) {
@@ -178,38 +208,96 @@ __device__ __forceinline__ double rounding_of_c(float m, float c, double inv_t) 
   return fabs(d) < 1e-5 ? 1.0 + d : exp(d);
 }
 
+// The blocks' records as the row's, by a whole warp, the result in lanes 0 to 15.
+__device__ __forceinline__ Record join_records(const Record* recs, int cluster) {
+  const int lane = threadIdx.x & 31;
+  Record t{0.0, 0.0, 0.0, 0.0, -INFINITY, -INFINITY, -INFINITY};
+  if (lane < cluster) t = recs[lane];
+  float n = t.n, tn = t.tn;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+    tn = fmaxf(tn, __shfl_xor_sync(0xffffffffu, tn, o));
+    t.m = fmaxf(t.m, __shfl_xor_sync(0xffffffffu, t.m, o));
+  }
+  t.s = t.n > -INFINITY ? t.s * pow2((double)t.n - (double)n) : 0.0;
+  t.ts = t.tn > -INFINITY ? t.ts * pow2((double)t.tn - (double)tn) : 0.0;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+    t.ts += __shfl_xor_sync(0xffffffffu, t.ts, o);
+    t.z += __shfl_xor_sync(0xffffffffu, t.z, o);
+    t.a += __shfl_xor_sync(0xffffffffu, t.a, o);
+  }
+  t.n = n;
+  t.tn = tn;
+  return t;
+}
+
+// What all of a block needs of a row.
+struct Row {
+  float n, coef;     // another column's gradient: coef * 2^(c z - n)
+  int live, guard;
+  double scale, P;   // w / T; the teacher's mass
+  double zn;         // p = exp(y - my) / zn
+  double all;        // S * 2^-tn_row ... of an entry: q = e * 2^(tn - tn_row) / all
+  float tn;
+};
+__device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, const Record& t) {
+  Row o{};
+  const double rest = t.s * rounding_of_c(t.m, a.c, a.inv_t);
+  o.live = live && (t.z > 0.0 || isnan(t.z)) && (t.s > 0.0 || t.ts > 0.0);
+  o.zn = a.d.teacher_lse ? 1.0 : t.z;
+  const double psum = a.d.teacher_lse ? t.z : 1.0;
+  const double rho = a.d.teacher_lse && t.s > 0.0 ? fmax(0.0, 1.0 - psum) : 0.0;
+  o.scale = (double)w * a.inv_t;
+  o.P = psum + rho;
+  o.n = t.n;
+  o.tn = t.tn;
+  const double gap = (double)t.n - (double)t.tn;  // infinite where one of them is
+  const double outside = t.ts > 0.0 ? rest / (rest + t.ts * pow2(-gap)) : 1.0;
+  o.coef = o.live && t.s > 0.0 ? (float)(o.scale * (o.P * outside - rho) / t.s) : 0.f;
+  o.all = t.ts + (t.s > 0.0 ? rest * pow2(gap) : 0.0);
+  o.guard = o.coef == 0.f || is_extreme(t.m);
+  return o;
+}
+
 // Loss and stats of a row: one thread of block 0.
-__device__ __forceinline__ void finish_row(const DistillArgs& a, int r, float w, const Top& t, const Part& p) {
-  const bool rest = p.s > 0.0;
-  const double l_rest = log_sum_exp(p.s, p.n, p.m, a.c, a.inv_t);
-  const double l_top = t.sum > 0.0 ? kLn2 * (log2(t.sum) + (double)t.ref) : -INFINITY;
-  const double hi = fmax(l_rest, l_top), lo = fmin(l_rest, l_top);
-  if (!t.live || !(hi > -INFINITY)) {
+__device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double my, const Record& t, const Row& o) {
+  if (!o.live) {
     a.loss[r] = 0.f;
     store_stats(a.stats, r, Stats{});
     return;
   }
+  const double l_rest = log_sum_exp(t.s, t.n, t.m, a.c, a.inv_t);
+  const double l_top = t.ts > 0.0 ? kLn2 * (log2(t.ts) + (double)t.tn) : -INFINITY;
+  const double hi = fmax(l_rest, l_top), lo = fmin(l_rest, l_top);
   const double L = hi + log1p(exp(lo - hi));
-  const double rho = a.d.teacher_lse && rest ? fmax(0.0, 1.0 - t.psum) : 0.0;
-  const double loss = t.lead + t.psum * L + (rho > 0.0 ? rho * (log(rho) - l_rest + L) : 0.0);
-  a.loss[r] = (float)((double)w * loss);
+  const double lp = a.d.teacher_lse ? my : my + log(t.z);
+  const double psum = a.d.teacher_lse ? t.z : 1.0, rho = o.P - psum;
+  const double loss = t.a / o.zn - psum * lp + psum * L + (rho > 0.0 ? rho * (log(rho) - l_rest + L) : 0.0);
+  a.loss[r] = (float)(o.scale / a.inv_t * loss);
   if (a.stats) {
-    const double scale = (double)w * a.inv_t, P = t.psum + rho;
     Stats st;
-    st.n = p.n;
-    st.rest = rest ? (float)(scale * (P * exp(l_rest - L) - rho) / p.s) : 0.f;
+    st.n = t.n;
+    st.rest = o.coef;
     st.l_hi = (float)L;
     st.l_lo = (float)(L - (double)st.l_hi);
-    st.all = (float)(scale * P);
-    st.scale = (float)scale;
-    st.lp_hi = (float)t.lp;
-    st.lp_lo = (float)(t.lp - (double)st.lp_hi);
+    st.all = (float)(o.scale * o.P);
+    st.scale = (float)o.scale;
+    st.lp_hi = (float)lp;
+    st.lp_lo = (float)(lp - (double)st.lp_hi);
     store_stats(a.stats, r, st);
   }
 }
 
-// The warps' sums (lane 0 of each holds its warp's) as the block's, in warp order; `warps` records.
-__device__ __forceinline__ void give_warp(DistillShared& sh, const ExpSum& acc, float m) {
+constexpr int kMaxWarps = 16;
+struct WarpSums {
+  double s[kMaxWarps];
+  float n[kMaxWarps], m[kMaxWarps];
+};
+// A warp's sum and maximum, to be joined by one warp.
+__device__ __forceinline__ void give_warp(WarpSums& ws, const ExpSum& acc, float m) {
   float n = acc.n;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -218,62 +306,48 @@ __device__ __forceinline__ void give_warp(DistillShared& sh, const ExpSum& acc, 
   }
   const double s = warp_add(n > -INFINITY ? (double)(acc.s * ex2(acc.n - n)) : 0.0);
   if ((threadIdx.x & 31) == 0) {
-    sh.red_n[threadIdx.x >> 5] = n;
-    sh.red_m[threadIdx.x >> 5] = m;
-    sh.red_s[threadIdx.x >> 5] = s;
+    ws.n[threadIdx.x >> 5] = n;
+    ws.m[threadIdx.x >> 5] = m;
+    ws.s[threadIdx.x >> 5] = s;
   }
 }
-__device__ __forceinline__ Part block_part(const DistillShared& sh, int warps) {
-  Part p{0.0, -INFINITY, -INFINITY};
-  for (int w = 0; w < warps; ++w) {
-    p.n = fmaxf(p.n, sh.red_n[w]);
-    p.m = fmaxf(p.m, sh.red_m[w]);
+// One warp: the block's record, in lanes 0 to 15.
+__device__ __forceinline__ Record block_record(const WarpSums& ws, int warps, const OwnSums& own) {
+  const int lane = threadIdx.x & 31;
+  const float mine = lane < warps ? ws.n[lane] : -INFINITY;
+  float n = mine, m = lane < warps ? ws.m[lane] : -INFINITY;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  for (int w = 0; w < warps; ++w)
-    if (sh.red_n[w] > -INFINITY) p.s += sh.red_s[w] * (double)ex2(sh.red_n[w] - p.n);
-  return p;
+  double s = mine > -INFINITY ? ws.s[lane] * pow2((double)mine - (double)n) : 0.0;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return Record{s, own.ts, own.z, own.a, n, m, own.tn};
 }
-// The blocks' parts as the row's.
-__device__ __forceinline__ Part row_part(const DistillShared& sh, int cluster) {
-  Part p{0.0, -INFINITY, -INFINITY};
-  for (int c = 0; c < cluster; ++c) {
-    p.n = fmaxf(p.n, sh.parts[c].n);
-    p.m = fmaxf(p.m, sh.parts[c].m);
-  }
-  for (int c = 0; c < cluster; ++c)
-    if (sh.parts[c].n > -INFINITY) p.s += sh.parts[c].s * (double)ex2(sh.parts[c].n - p.n);
-  return p;
-}
-__device__ __forceinline__ void send_part(DistillShared& sh, uint32_t rank, uint32_t to, const Part& p) {
-  const uint32_t at = cluster_address(&sh.parts[rank], to);
-  cluster_store(at, p.s);
-  cluster_store(at + 8, p.n, p.m);
-}
-// Block 0's top to another block.
-__device__ __forceinline__ void send_top(DistillShared& sh, uint32_t to) {
-  const uint32_t at = cluster_address(&sh.top, to);
-  const Top& t = sh.top;
-  cluster_store(at, t.sum);
-  cluster_store(at + 8, t.psum);
-  cluster_store(at + 16, t.lp);
-  cluster_store(at + 24, t.lead);
-  cluster_store(at + 32, __float_as_int(t.ref));
-  cluster_store(at + 36, t.live);
-  cluster_store(at + 40, t.twice);
+__device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const Record& t) {
+  const uint32_t at = cluster_address(to_slot, to);
+  cluster_store(at, t.s);
+  cluster_store(at + 8, t.ts);
+  cluster_store(at + 16, t.z);
+  cluster_store(at + 24, t.a);
+  cluster_store(at + 32, t.n, t.m);
+  cluster_store(at + 40, __float_as_int(t.tn));
 }
 
 // The columns that the entries' warp has set a bit for, of the vector `vec` of a slice, as a mask of its elements.
 __device__ __forceinline__ uint32_t marked(const uint32_t* marks, int vec) {
   return (marks[vec >> 2] >> ((vec & 3) * 8)) & 0xffu;
 }
-// Clears the marks of `vecs` vectors and sets those of the entries in them; the entries' warp alone.
+// Clears the marks of `vecs` vectors and sets those of the block's entries; one warp.
 template <int N>
-__device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, const Entries& en, int K) {
+__device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, const Own& own) {
   for (int i = threadIdx.x & 31; i < (vecs + 3) / 4; i += 32) marks[i] = 0;
   __syncwarp();
-  for (int k = threadIdx.x & 31; k < K; k += 32) {
-    const int id = en.id[k], vec = id / N - first;
-    if (id >= 0 && vec >= 0 && vec < vecs) atomicOr(&marks[vec >> 2], 1u << ((vec & 3) * 8 + id % N));
+  for (int k = threadIdx.x & 31; k < own.n; k += 32) {
+    const int vec = own.id[k] / N - first;
+    atomicOr(&marks[vec >> 2], 1u << ((vec & 3) * 8 + own.id[k] % N));
   }
 }
 
@@ -289,44 +363,6 @@ template <typename T>
 __device__ __forceinline__ uint32_t beyond(int v, int V) {  // mask of the vector at column v
   return v + Vec<T>::N <= V ? 0u : v >= V ? 0xffu : 0xffu << (V - v);
 }
-// Adds the first `vecs` of a thread's NV vectors, of maximum m > -infinity, to its sum; true where a value is NaN or
-// the terms need a guard.
-template <typename T, int NV>
-__device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], int vecs, float m, float c) {
-  const float n = fmaxf(a.n, reference_of(m, c));
-  if (n > a.n) raise(a, n);
-  float2 s = make_float2(0.f, 0.f);
-  if (!is_extreme(m)) {
-    const float2 c2 = make_float2(c, c), n2 = make_float2(-n, -n);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i >= vecs) break;
-      float z[Vec<T>::N];
-      widen(q[i], z);
-#pragma unroll
-      for (int e = 0; e < Vec<T>::N; e += 2) {
-        const float2 x = fma2(make_float2(z[e], z[e + 1]), c2, n2);
-        s = add2(s, make_float2(ex2(x.x), ex2(x.y)));
-      }
-    }
-  }
-  float t = s.x + s.y;
-  const bool guard = is_extreme(m) || isnan(t);
-  if (guard) {
-    t = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i >= vecs) break;
-      float z[Vec<T>::N];
-      widen(q[i], z);
-#pragma unroll
-      for (int e = 0; e < Vec<T>::N; ++e) t += term_guarded(z[e], c, n);
-    }
-  }
-  a.s += t;
-  return guard;
-}
-
 __device__ __forceinline__ void store_grad(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_grad(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -346,7 +382,6 @@ __device__ __forceinline__ void write_vector(G* out, int v, int V, const uint4& 
       z[e + 1] = y.y;
     }
   } else {
-#pragma unroll
     for (int e = 0; e < N; ++e) z[e] = coef == 0.f ? 0.f : coef * term_guarded(z[e], c, n);
   }
   if (v + N <= V) {
@@ -368,216 +403,148 @@ __device__ __forceinline__ void write_vector(G* out, int v, int V, const uint4& 
   }
 }
 
-// The entries' warp: f(entry, column, p) for the entries with columns in [v0, v1), once a token with the sum of its
-// entries' p.
-template <typename F>
-__device__ __forceinline__ void each_own(int K, Entries& en, int v0, int v1, double lp, bool twice, F f) {
-  const int lane = threadIdx.x & 31;
-  if (twice) {
-    for (int k = lane; k < K; k += 32) en.p[k] = en.y[k] > -INFINITY ? exp(en.y[k] - lp) : 0.0;
-    __syncwarp();
-  }
-  for (int k = lane; k < K; k += 32) {
-    const int id = en.id[k];
-    if (id < v0 || id >= v1) continue;  // -1 too
-    double p = 0.0;
-    bool first = true;
-    if (twice) {
-      for (int j = 0; j < K; ++j)
-        if (en.id[j] == id) {
-          p += en.p[j];
-          first &= j >= k;
-        }
-    } else if (en.y[k] > -INFINITY) {
-      p = exp(en.y[k] - lp);
-    }
-    if (first) f(k, id, p);
-  }
-}
+// Named barriers of a block, for warps that go different ways (0 is __syncthreads): `n` threads arrive or wait.
+template <int ID> __device__ __forceinline__ void bar_arrive(int n) { asm volatile("bar.arrive %0, %1;" ::"n"(ID), "r"(n) : "memory"); }
+template <int ID> __device__ __forceinline__ void bar_wait(int n) { asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(n) : "memory"); }
 
-// Loss and gradient of one row a cluster, held in registers: kNV vectors of each of THREADS - 32 threads; the last
-// warp has the entries.
+// Loss, and gradient (G not void), of one row a cluster.  Data warps stream the slice, the next tile's loads in
+// flight while one is worked on; one warp has the entries and the exchange.
 //
-// Bound by memory: V values read and V written a row.  One exponential for the sum and one for the gradient
-// (16 a clock and SM) take half of the memory's time for bf16 in and out.
-template <typename T, typename G, int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill_row(DistillArgs a) {
-  constexpr int N = Vec<T>::N, DATA = THREADS - 32, WARPS = DATA / 32;
-  __shared__ DistillShared sh;
-  __shared__ uint32_t marks[(DATA * NV + 3) / 4];
-  pdl_wait();
-  pdl_trigger();
-  const domino_distill_t& d = a.d;
-  const int cluster = a.cluster, r = blockIdx.x / cluster, tid = threadIdx.x;
-  const uint32_t rank = blockIdx.x % cluster;
-  const bool entries = tid >= DATA;
-  const int all = (d.V + N - 1) / N, per = (all + cluster - 1) / cluster;
-  const int first = min((int)rank * per, all), last = min(first + per, all);
-  const int vecs = (last - first + DATA - 1) / DATA;  // <= NV
-  G* out = static_cast<G*>(a.grad) + (size_t)r * a.grad_ld;
-  const float w = d.row_weights ? d.row_weights[r] : 1.f;
-  const T* row = static_cast<const T*>(d.logits) + (size_t)r * d.ld;
-  uint4 q[NV];
-  if (w == 0.f) {  // the whole cluster
-    if (!entries) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int vec = first + i * DATA + tid;
-        if (vec < last) write_vector<T>(out, vec * N, d.V, barred_vec<T>(), a.c, 0.f, 0.f, true);
-      }
-    } else if (rank == 0 && tid == DATA) {
-      a.loss[r] = 0.f;
-      store_stats(a.stats, r, Stats{});
-    }
-    return;
-  }
-  cluster_arrive();  // all blocks have started before one stores into another
-  if (!entries) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int vec = first + i * DATA + tid;
-      q[i] = vec < last ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
-    }
-  } else {
-    load_entries(a, r, row, rank == 0 ? 0 : first * N, rank == 0 ? d.V : last * N, sh.en, rank == 0);
-    set_marks<N>(marks, first, last - first, sh.en, d.K);
-  }
-  __syncthreads();  // marks are set
-  bool guard = false;
-  if (!entries) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i >= vecs) break;
-      const int vec = i * DATA + tid;
-      if (first + vec < last) {
-        const uint32_t mask = marked(marks, vec) | beyond<T>((first + vec) * N, d.V);
-        if (mask) bar<T>(q[i], mask);
-      }
-      m = fmaxf(m, vec_max(q[i], T()));
-    }
-    ExpSum acc;
-    if (m > -INFINITY) guard = add_vectors<T, NV>(acc, q, vecs, m, a.c);
-    give_warp(sh, acc, m);
-  } else if (rank == 0) {
-    find_top(a, r, sh);
-  }
-  __syncthreads();
-  cluster_wait();
-  if (tid < cluster) send_part(sh, rank, tid, block_part(sh, WARPS));
-  if (rank == 0 && tid > DATA && tid - DATA < cluster) send_top(sh, tid - DATA);
-  cluster_arrive();
-  cluster_wait();
-  const Part part = row_part(sh, cluster);
-  const Top& t = sh.top;
-  const double scale = (double)w * a.inv_t;
-  const double rest = part.s * rounding_of_c(part.m, a.c, a.inv_t);
-  const double rho = d.teacher_lse && rest > 0.0 ? fmax(0.0, 1.0 - t.psum) : 0.0, P = t.psum + rho;
-  const double gap = part.s > 0.0 ? (double)part.n - (double)t.ref : -2000.0;
-  const bool live = t.live && (part.s > 0.0 || t.sum > 0.0);
-  if (!entries) {
-    // rest / (rest + top): what of S lies outside the entries
-    const double outside = rest / (rest + t.sum * pow2(-gap));
-    const float coef = live && part.s > 0.0 ? (float)(scale * (P * outside - rho) / part.s) : 0.f;
-    guard |= coef == 0.f || is_extreme(part.m);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i >= vecs) break;
-      const int vec = first + i * DATA + tid;
-      if (vec < last) write_vector<T>(out, vec * N, d.V, q[i], a.c, part.n, coef, guard);
-    }
-  }
-  __syncthreads();  // the entries' columns go over the others'
-  if (entries) {
-    if (live) {
-      const double s = t.sum + (part.s > 0.0 ? rest * pow2(gap) : 0.0);
-      each_own(d.K, sh.en, first * N, last * N, t.lp, t.twice, [&](int k, int v, double p) {
-        const double q_v = sh.en.x[k] > -INFINITY ? exp2(sh.en.x[k] * kLog2e - (double)t.ref) / s : 0.0;
-        store_grad(out + v, (float)(scale * (P * q_v - p)));
-      });
-    }
-    if (rank == 0 && tid == DATA) finish_row(a, r, w, t, part);
-  }
-}
+// Bound by memory: V values read once from DRAM and V written.  The second read hits L2 as long as the rows in work
+// take less than about half of it, which the launch sees to with the cluster's size.  (Holding a row in
+// registers or shared memory between the two took longer: 231 us and 346 us where this takes NNN, 1024 rows of
+// 151936 bf16.)
+constexpr int kThreads = 256;
+constexpr int kData = kThreads - 32;
+constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
+constexpr int kSlice = 24576;     // vectors of a slice at most: a byte of marks each
 
-// A row's sums by a cluster that reads it once, for the loss and the stats.  The marks take a byte a vector of the
-// slice.
-constexpr int kSumThreads = 256;
-constexpr int kSumVecs = 4;
-constexpr int kSumSlice = 24576;  // vectors of a slice at most
-
-template <typename T>
-__global__ void __launch_bounds__(kSumThreads, 4) k_distill_sum(DistillArgs a) {
-  constexpr int N = Vec<T>::N, DATA = kSumThreads - 32, WARPS = DATA / 32;
-  __shared__ DistillShared sh;
+template <typename T, typename G>
+__global__ void __launch_bounds__(kThreads, 4) k_distill(DistillArgs a) {
+  constexpr int N = Vec<T>::N;
+  constexpr bool kGrad = !std::is_void<G>::value;
+  __shared__ struct {
+    Record recs[kMaxCluster];
+    Own own;
+    OwnSums sums;
+    WarpSums warps;
+    Row row;
+  } sh;
   extern __shared__ uint32_t marks[];
   pdl_wait();
   pdl_trigger();
   const domino_distill_t& d = a.d;
   const int cluster = a.cluster, r = blockIdx.x / cluster, tid = threadIdx.x;
   const uint32_t rank = blockIdx.x % cluster;
-  const bool entries = tid >= DATA;
   const int all = (d.V + N - 1) / N, per = (all + cluster - 1) / cluster;
   const int first = min((int)rank * per, all), last = min(first + per, all);
   const float w = d.row_weights ? d.row_weights[r] : 1.f;
   const T* row = static_cast<const T*>(d.logits) + (size_t)r * d.ld;
+  using Out = typename std::conditional<kGrad, G, float>::type;
+  Out* out = kGrad ? static_cast<Out*>(a.grad) + (size_t)r * a.grad_ld : nullptr;
   if (w == 0.f) {  // the whole cluster
+    if constexpr (kGrad) {
+      for (int vec = first + tid; vec < last; vec += kThreads)
+        write_vector<T>(out, vec * N, d.V, barred_vec<T>(), a.c, 0.f, 0.f, true);
+    }
     if (rank == 0 && tid == 0) {
       a.loss[r] = 0.f;
       store_stats(a.stats, r, Stats{});
     }
     return;
   }
-  cluster_arrive();
-  constexpr int kTile = DATA * kSumVecs;
-  auto load = [&](uint4(&q)[kSumVecs], int t0) {
+  cluster_arrive();  // all blocks have started before one stores into another
+  if (tid < kData) {
+    constexpr int kTile = kData * kVecs;
+    auto load = [&](uint4(&q)[kVecs], int t0) {
 #pragma unroll
-    for (int i = 0; i < kSumVecs; ++i) {
-      const int vec = t0 + i * DATA + tid;
-      q[i] = vec < last ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
-    }
-  };
-  uint4 next[kSumVecs];
-  if (!entries) {
+      for (int i = 0; i < kVecs; ++i) {
+        const int vec = t0 + i * kData + tid;
+        const uint4* at = reinterpret_cast<const uint4*>(row) + vec;
+        q[i] = vec < last ? (kGrad ? __ldcg(at) : __ldcs(at)) : barred_vec<T>();
+      }
+    };
+    uint4 next[kVecs];
     load(next, first);
-  } else {
-    load_entries(a, r, row, 0, rank == 0 ? d.V : 0, sh.en, rank == 0);
-    set_marks<N>(marks, first, last - first, sh.en, d.K);
-  }
-  __syncthreads();
-  if (!entries) {
+    bar_wait<1>(kThreads);  // the marks are set
     ExpSum acc;
     float m = -INFINITY;
+    bool guard = false;
     for (int t0 = first; t0 < last; t0 += kTile) {
-      uint4 q[kSumVecs];
+      uint4 q[kVecs];
 #pragma unroll
-      for (int i = 0; i < kSumVecs; ++i) q[i] = next[i];
+      for (int i = 0; i < kVecs; ++i) q[i] = next[i];
       load(next, t0 + kTile);
       float tm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kSumVecs; ++i) {
-        const int vec = t0 + i * DATA + tid;
+      for (int i = 0; i < kVecs; ++i) {
+        const int vec = t0 + i * kData + tid;
         if (vec < last) {
           const uint32_t mask = marked(marks, vec - first) | beyond<T>(vec * N, d.V);
           if (mask) bar<T>(q[i], mask);
         }
         tm = fmaxf(tm, vec_max(q[i], T()));
       }
-      if (tm > -INFINITY) {
-        m = fmaxf(m, tm);
-        add_vectors<T, kSumVecs>(acc, q, kSumVecs, tm, a.c);
-      }
+      m = fmaxf(m, tm);
+      guard |= add_vectors<T>(acc, q, tm, a.c);
     }
-    give_warp(sh, acc, m);
-  } else if (rank == 0) {
-    find_top(a, r, sh);
+    give_warp(sh.warps, acc, m);
+    bar_arrive<2>(kThreads);  // sh.warps
+    if (kGrad) load(next, first);
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    if constexpr (kGrad) {
+      bar_wait<1>(kThreads);  // sh.row
+      const float n = sh.row.n, coef = sh.row.coef;
+      guard |= sh.row.guard != 0;
+      for (int t0 = first; t0 < last; t0 += kTile) {
+        uint4 q[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) q[i] = next[i];
+        load(next, t0 + kTile);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const int vec = t0 + i * kData + tid;
+          if (vec < last) write_vector<T>(out, vec * N, d.V, q[i], a.c, n, coef, guard);
+        }
+      }
+      bar_arrive<2>(kThreads);  // the entries' columns go over the others'
+    }
+    return;
   }
-  __syncthreads();
+  const int lane = tid & 31;
+  find_own(a, r, first * N, last * N, sh.own, rank == 0);
+  set_marks<N>(marks, first, last - first, sh.own);
+  bar_wait<1>(kThreads);  // the marks are set
+  sum_own(a, sh.own, row, sh.sums);
+  bar_wait<2>(kThreads);  // sh.warps
+  const Record rec = block_record(sh.warps, kData / 32, sh.sums);
   cluster_wait();
-  if (tid == 0) send_part(sh, rank, 0, block_part(sh, WARPS));
+  if (lane < (kGrad ? cluster : 1)) send_record(&sh.recs[rank], lane, rec);
+  __syncwarp();
   cluster_arrive();
   cluster_wait();
-  if (rank == 0 && tid == DATA) finish_row(a, r, w, sh.top, row_part(sh, cluster));
+  if (!kGrad && rank != 0) return;
+  const Record t = join_records(sh.recs, cluster);
+  const Row o = row_of(a, w, sh.own.live, t);
+  if constexpr (kGrad) {
+    if (lane == 0) sh.row = o;
+    bar_wait<1>(kThreads);
+  }
+  if (rank == 0 && lane == 0) finish_row(a, r, sh.own.my, t, o);
+  if constexpr (kGrad) {
+    bar_wait<2>(kThreads);
+    if (sh.row.live) {
+      const Row& whole = sh.row;
+      const double to_row = pow2((double)sh.sums.tn - (double)whole.tn) / whole.all, of_teacher = 1.0 / whole.zn;
+      for (int k = lane; k < sh.own.n; k += 32)
+        if (sh.sums.p[k] >= 0.f) {
+          const double q_v = sh.sums.e[k] > 0.f ? (double)sh.sums.e[k] * to_row : 0.0;
+          store_grad(out + sh.own.id[k], (float)(whole.scale * (whole.P * q_v - (double)sh.sums.p[k] * of_teacher)));
+        }
+    }
+  }
 }
 
 // The gradient from a row's stats, a chunk of kGradVecs vectors a thread by each block.  The logits may be
@@ -588,9 +555,9 @@ constexpr int kGradVecs = 8;
 template <typename T, typename G>
 __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ Entries en;
-  __shared__ float own[kMaxK];  // an entry's gradient, where it is this chunk's to write
-  __shared__ int at[kMaxK];     // ... and its column, else -1
+  __shared__ Own own;
+  __shared__ float grads[kMaxK];  // an entry's gradient, where it is the first of its token's
+  __shared__ bool firsts[kMaxK];
   pdl_wait();
   pdl_trigger();
   const domino_distill_t& d = a.d;
@@ -608,15 +575,20 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
     q[i] = live && vec < all ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
   }
   if (tid < 32 && live) {
-    const int v0 = first * N, v1 = min(first + kGradThreads * kGradVecs, all) * N;
-    load_entries(a, r, row, v0, v1, en, false);
-    for (int k = tid; k < d.K; k += 32) at[k] = -1;
+    find_own(a, r, first * N, min(first + kGradThreads * kGradVecs, all) * N, own, false);
     const double lp = (double)st.lp_hi + (double)st.lp_lo, L = (double)st.l_hi + (double)st.l_lo;
-    each_own(d.K, en, v0, v1, lp, true, [&](int k, int v, double p) {
-      const double q_v = en.x[k] > -INFINITY ? exp(en.x[k] - L) : 0.0;
-      own[k] = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
-      at[k] = v;
-    });
+    for (int k = tid; k < own.n; k += 32) {
+      double p = 0.0;
+      firsts[k] = true;
+      for (int j = 0; j < own.n; ++j)
+        if (own.id[j] == own.id[k]) {
+          if (own.y[j] > -INFINITY) p += exp(own.y[j] - lp);
+          if (j < k) firsts[k] = false;
+        }
+      const float z = to_f32(row[own.id[k]]);
+      const double q_v = z > -INFINITY ? exp((double)big_clamp(z) * a.inv_t - L) : 0.0;
+      grads[k] = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
+    }
   }
   __syncthreads();  // the entries' logits are read
   const float coef = live ? g * st.rest : 0.f;
@@ -627,21 +599,30 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
     if (vec < all) write_vector<T>(out, vec * N, d.V, q[i], a.c, st.n, coef, true);
   }
   __syncthreads();
-  if (live && tid < d.K && at[tid] >= 0) store_grad(out + at[tid], own[tid]);
+  if (live && tid < own.n && firsts[tid]) store_grad(out + own.id[tid], grads[tid]);
 }
 
 int vectors_of(const domino_distill_t& d) { return d.dtype == DOMINO_DTYPE_F32 ? (d.V + 3) / 4 : (d.V + 7) / 8; }
 
-cudaError_t launch_sum(DistillArgs a, cudaStream_t st) {
+// Loss, and gradient where a.grad is set.
+cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
   const int vecs = vectors_of(a.d);
+  const int64_t blocks = 4 * 148;  // at a time
+  const bool f = a.d.dtype == DOMINO_DTYPE_F32;
   int cluster = 1;
-  while (cluster < kMaxCluster && (vecs > cluster * kSumSlice || ((int64_t)a.d.rows * cluster < 4 * 148 &&
-                                                                  vecs / (2 * cluster) >= 2 * kSumThreads)))
+  // larger clusters: for slices that have their marks in shared memory; where few rows would leave SMs idle; and
+  // to keep the rows in work in about 48 MB of L2
+  while (cluster < kMaxCluster &&
+         (vecs > cluster * kSlice || (a.d.rows * (int64_t)cluster < blocks && vecs / (2 * cluster) >= 2 * kData) ||
+          (a.grad && std::min<int64_t>(a.d.rows, blocks / cluster) * vecs * 16 > (48 << 20) && vecs / (2 * cluster) >= 2 * kData)))
     cluster *= 2;
   a.cluster = cluster;
   const size_t smem = ((vecs + cluster - 1) / cluster + 3) / 4 * 4;
-  auto kern = a.d.dtype == DOMINO_DTYPE_F32 ? k_distill_sum<float> : k_distill_sum<bf16>;
-  return note_launch(launch_cluster(kern, cluster, dim3((unsigned)a.d.rows * (unsigned)cluster), dim3(kSumThreads), smem,
+  const bool g = grad_dtype == DOMINO_DTYPE_F32;
+  auto kern = !a.grad ? (f ? k_distill<float, void> : k_distill<bf16, void>)
+                      : f ? (g ? k_distill<float, float> : k_distill<float, bf16>)
+                          : (g ? k_distill<bf16, float> : k_distill<bf16, bf16>);
+  return note_launch(launch_cluster(kern, cluster, dim3((unsigned)a.d.rows * (unsigned)cluster), dim3(kThreads), smem,
                                     st, a));
 }
 
@@ -651,30 +632,6 @@ cudaError_t launch_grad(DistillArgs a, int grad_dtype, cudaStream_t st) {
   auto kern = f ? (g ? k_distill_grad<float, float> : k_distill_grad<float, bf16>)
                 : (g ? k_distill_grad<bf16, float> : k_distill_grad<bf16, bf16>);
   return note_launch(launch_pdl(kern, dim3((unsigned)a.d.rows * (unsigned)a.cluster), dim3(kGradThreads), 0, st, a));
-}
-
-template <typename T, typename G>
-constexpr int row_threads() { return sizeof(T) == 4 ? 512 : 256; }
-template <typename T, typename G>
-constexpr int row_vecs() { return sizeof(T) == 4 ? 10 : 11; }
-
-// Whether a cluster holds a row; the smallest cluster that does.
-template <typename T, typename G>
-cudaError_t launch_row_as(DistillArgs a, cudaStream_t st, bool* held) {
-  constexpr int threads = row_threads<T, G>(), block = (threads - 32) * row_vecs<T, G>();
-  const int vecs = vectors_of(a.d);
-  int cluster = 1;
-  while (cluster < kMaxCluster && vecs > cluster * block) cluster *= 2;
-  *held = vecs <= cluster * block;
-  if (!*held) return cudaSuccess;
-  a.cluster = cluster;
-  return note_launch(launch_cluster(k_distill_row<T, G, threads, row_vecs<T, G>()>, cluster,
-                                    dim3((unsigned)a.d.rows * (unsigned)cluster), dim3(threads), 0, st, a));
-}
-cudaError_t launch_row(const DistillArgs& a, int grad_dtype, cudaStream_t st, bool* held) {
-  const bool f = a.d.dtype == DOMINO_DTYPE_F32, g = grad_dtype == DOMINO_DTYPE_F32;
-  return f ? (g ? launch_row_as<float, float>(a, st, held) : launch_row_as<float, bf16>(a, st, held))
-           : (g ? launch_row_as<bf16, float>(a, st, held) : launch_row_as<bf16, bf16>(a, st, held));
 }
 
 int check_distill(const domino_distill_t* d) {
@@ -736,13 +693,7 @@ extern "C" int domino_distill(const domino_distill_t* args, float* loss, float* 
   a.grad = grad;
   a.grad_ld = grad_ld;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  bool held = false;
-  cudaError_t e = cudaSuccess;
-  if (grad) e = launch_row(a, grad_dtype, cs, &held);
-  if (e == cudaSuccess && !held) {
-    e = launch_sum(a, cs);
-    if (e == cudaSuccess && grad) e = launch_grad(a, grad_dtype, cs);
-  }
+  const cudaError_t e = launch_distill(a, grad_dtype, cs);
   return e == cudaSuccess ? DOMINO_OK : DOMINO_ERR_CUDA;
 }
 

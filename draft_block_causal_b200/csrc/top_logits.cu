@@ -59,39 +59,6 @@ __device__ __forceinline__ uint4 cut_vec(uint4 q, int v, int V) {
   return q;
 }
 
-// Adds a tile with maximum m > -infinity to the thread's sum.
-template <typename T>
-__device__ __forceinline__ void add_tile(ExpSum& a, const uint4 (&q)[kVecs], float m, float c) {
-  const float n = fmaxf(a.n, reference_of(m, c));
-  if (n > a.n) raise(a, n);
-  float2 s = make_float2(0.f, 0.f);
-  if (!is_extreme(m)) {
-    const float2 c2 = make_float2(c, c), n2 = make_float2(-n, -n);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      float z[Vec<T>::N];
-      widen(q[i], z);
-#pragma unroll
-      for (int e = 0; e < Vec<T>::N; e += 2) {
-        const float2 x = fma2(make_float2(z[e], z[e + 1]), c2, n2);
-        s = add2(s, make_float2(ex2(x.x), ex2(x.y)));
-      }
-    }
-  }
-  float t = s.x + s.y;
-  if (is_extreme(m) || isnan(t)) {
-    t = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      float z[Vec<T>::N];
-      widen(q[i], z);
-#pragma unroll
-      for (int e = 0; e < Vec<T>::N; ++e) t += term_guarded(z[e], c, n);
-    }
-  }
-  a.s += t;
-}
-
 // Block 0's thread 0 gets sums over the block's threads.
 __device__ __forceinline__ void join_threads(const ExpSum& a, float m, TopShared& sh, double* sum, float* ref, float* max) {
   float n = a.n, mm = m;
@@ -277,10 +244,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
         vm[i] = fmaxf(vec_max(q[i], T()), -INFINITY);
         tm = fmaxf(tm, vm[i]);
       }
-      if (tm > -INFINITY) {
-        m = fmaxf(m, tm);
-        add_tile<T>(acc, q, tm, a.c);
-      }
+      m = fmaxf(m, tm);
+      add_vectors<T>(acc, q, tm, a.c);
       if (bar == 0 && can_bar) {  // no bar yet: this tile's columns may be the lowest that reach it
         bar = reached_by(order_of(m), warps, a.k, sh);
         floor = floor_at(bar);

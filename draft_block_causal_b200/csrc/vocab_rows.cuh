@@ -93,6 +93,41 @@ __device__ __forceinline__ void raise(ExpSum& a, float n) {
   a.n = n;
 }
 
+// Adds vectors of maximum m (NaN aside) to a thread's sum; true where their terms need a guard.  The reference is
+// raised only when a term would exceed 2^kSlack of it, so that it hardly ever is after the first vectors.
+constexpr float kSlack = 40.f;
+template <typename T, int NV>
+__device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], float m, float c) {
+  if (!(m > -INFINITY)) return false;
+  if (fmaf(big_clamp(m), c, -a.n) > kSlack) raise(a, reference_of(m, c));
+  float2 s = make_float2(0.f, 0.f);
+  const float2 c2 = make_float2(c, c), n2 = make_float2(-a.n, -a.n);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float z[Vec<T>::N];
+    widen(q[i], z);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; e += 2) {
+      const float2 x = fma2(make_float2(z[e], z[e + 1]), c2, n2);
+      s = add2(s, make_float2(ex2(x.x), ex2(x.y)));
+    }
+  }
+  float t = s.x + s.y;
+  const bool guard = is_extreme(m) || isnan(t);
+  if (guard) {
+    t = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float z[Vec<T>::N];
+      widen(q[i], z);
+#pragma unroll
+      for (int e = 0; e < Vec<T>::N; ++e) t += term_guarded(z[e], c, a.n);
+    }
+  }
+  a.s += t;
+  return guard;
+}
+
 // Order-preserving map of a logit onto 32 bits: larger is larger, -0 equals +0; NaN and -infinity, which
 // are never selected, are 0.
 __device__ __forceinline__ uint32_t order_of(float z) {
