@@ -70,6 +70,7 @@ struct Record {
 struct Own {
   int n;             // how many
   int live;          // the teacher's row counts
+  int twice;         // a token may be among them twice
   double my;         // what y is taken from: teacher_lse, or the row's largest y
   int32_t id[kMaxK];
   double y[kMaxK];
@@ -83,11 +84,6 @@ struct OwnSums {
   double ts, z, a;   // as in Record
 };
 
-__device__ __forceinline__ double warp_add(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 // One warp: a row's entries, one k = 32 i + lane after the other, for the block with columns [v0, v1).  Ends with the
 // warp's barrier.
 __device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, int v1, Own& own, bool report) {
@@ -139,13 +135,16 @@ __device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, in
   __syncwarp();
 }
 
-// 2^(difference of references): no power of two that a term could see is left out.
-__device__ __forceinline__ double pow2(double e) { return e < -1000.0 ? 0.0 : e > 1000.0 ? INFINITY : ldexp(1.0, (int)e); }
+// 2^e of a whole number: 0 below 2^-1022, infinity above 2^1023.
+__device__ __forceinline__ double pow2(double e) {
+  const int n = (int)fmin(fmax(e, -1023.0), 1024.0);
+  return __hiloint2double((n + 1023) << 20, 0);
+}
 
 // 2^t of a number in 64 bits: its whole part is exact, the rest goes through the fp32 exponential, 2^-22.
 __device__ __forceinline__ double exp2_near(double t) {
   const double n = rint(t);
-  return n < -1000.0 ? 0.0 : ldexp((double)ex2((float)(t - n)), (int)fmin(n, 1000.0));
+  return (double)ex2((float)(t - n)) * pow2(n);
 }
 
 // One warp: the sums over a block's entries, from their logits in `row`.
@@ -175,11 +174,12 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, co
     double p = pt;
     const double e = x > -INFINITY ? exp2_near(x * kLog2e - (double)tn) : 0.0;
     bool first = true;
-    for (int j = 0; j < n; ++j)
-      if (own.id[j] == id && j != k) {  // rare: a token given twice
-        first &= j > k;
-        if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - own.my) * kLog2e);
-      }
+    if (own.twice)
+      for (int j = 0; j < n; ++j)
+        if (own.id[j] == id && j != k) {
+          first &= j > k;
+          if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - own.my) * kLog2e);
+        }
     sums.e[k] = (float)e;
     sums.p[k] = first ? (float)p : -1.f;
     if (first) ts += e;
@@ -240,7 +240,8 @@ struct Row {
   int live, guard;
   double scale, P;   // w / T; the teacher's mass
   double zn;         // p = exp(y - my) / zn
-  double all;        // S * 2^-tn_row ... of an entry: q = e * 2^(tn - tn_row) / all
+  double all;        // S * 2^-tn: an entry's q = e * 2^(its tn - tn) / all
+  double outside;    // what of S lies outside the entries
   float tn;
 };
 __device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, const Record& t) {
@@ -255,8 +256,8 @@ __device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, c
   o.n = t.n;
   o.tn = t.tn;
   const double gap = (double)t.n - (double)t.tn;  // infinite where one of them is
-  const double outside = t.ts > 0.0 ? rest / (rest + t.ts * pow2(-gap)) : 1.0;
-  o.coef = o.live && t.s > 0.0 ? (float)(o.scale * (o.P * outside - rho) / t.s) : 0.f;
+  o.outside = t.ts > 0.0 ? rest / (rest + t.ts * pow2(-gap)) : 1.0;
+  o.coef = o.live && t.s > 0.0 ? (float)(o.scale * (o.P * o.outside - rho) / t.s) : 0.f;
   o.all = t.ts + (t.s > 0.0 ? rest * pow2(gap) : 0.0);
   o.guard = o.coef == 0.f || is_extreme(t.m);
   return o;
@@ -269,13 +270,13 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double m
     store_stats(a.stats, r, Stats{});
     return;
   }
-  const double l_rest = log_sum_exp(t.s, t.n, t.m, a.c, a.inv_t);
-  const double l_top = t.ts > 0.0 ? kLn2 * (log2(t.ts) + (double)t.tn) : -INFINITY;
-  const double hi = fmax(l_rest, l_top), lo = fmin(l_rest, l_top);
-  const double L = hi + log1p(exp(lo - hi));
+  // L from the entries' reference unless the others' sum is beyond it; log tau = log outside unless that is too small
+  const bool from_top = t.ts > 0.0 && o.all < 1e300;
+  const double l_rest = !from_top || o.outside < 1e-300 ? log_sum_exp(t.s, t.n, t.m, a.c, a.inv_t) : 0.0;
+  const double L = from_top ? kLn2 * (log2(o.all) + (double)t.tn) : l_rest;
   const double lp = a.d.teacher_lse ? my : my + log(t.z);
   const double psum = a.d.teacher_lse ? t.z : 1.0, rho = o.P - psum;
-  const double loss = t.a / o.zn - psum * lp + psum * L + (rho > 0.0 ? rho * (log(rho) - l_rest + L) : 0.0);
+  const double loss = t.a / o.zn - psum * lp + psum * L + (rho > 0.0 ? rho * (o.outside < 1e-300 ? log(rho) - l_rest + L : log(rho / o.outside)) : 0.0);
   a.loss[r] = (float)(o.scale / a.inv_t * loss);
   if (a.stats) {
     Stats st;
@@ -293,10 +294,9 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double m
 
 constexpr int kMaxWarps = 16;
 struct WarpSums {
-  double s[kMaxWarps];
-  float n[kMaxWarps], m[kMaxWarps];
+  float s[kMaxWarps], n[kMaxWarps], m[kMaxWarps];
 };
-// A warp's sum and maximum, to be joined by one warp.
+// A warp's sum, in fp32, and maximum; the warps' are joined by one of them in 64 bits.
 __device__ __forceinline__ void give_warp(WarpSums& ws, const ExpSum& acc, float m) {
   float n = acc.n;
 #pragma unroll
@@ -304,7 +304,7 @@ __device__ __forceinline__ void give_warp(WarpSums& ws, const ExpSum& acc, float
     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  const double s = warp_add(n > -INFINITY ? (double)(acc.s * ex2(acc.n - n)) : 0.0);
+  const float s = warp_sum(n > -INFINITY ? acc.s * ex2(acc.n - n) : 0.f);
   if ((threadIdx.x & 31) == 0) {
     ws.n[threadIdx.x >> 5] = n;
     ws.m[threadIdx.x >> 5] = m;
@@ -321,7 +321,7 @@ __device__ __forceinline__ Record block_record(const WarpSums& ws, int warps, co
     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  double s = mine > -INFINITY ? ws.s[lane] * pow2((double)mine - (double)n) : 0.0;
+  double s = mine > -INFINITY ? (double)ws.s[lane] * pow2((double)mine - (double)n) : 0.0;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return Record{s, own.ts, own.z, own.a, n, m, own.tn};
@@ -336,39 +336,37 @@ __device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const 
   cluster_store(at + 40, __float_as_int(t.tn));
 }
 
-// The columns that the entries' warp has set a bit for, of the vector `vec` of a slice, as a mask of its elements.
-__device__ __forceinline__ uint32_t marked(const uint32_t* marks, int vec) {
-  return (marks[vec >> 2] >> ((vec & 3) * 8)) & 0xffu;
-}
-// Clears the marks of `vecs` vectors and sets those of the block's entries; one warp.
+// Marks: a word for each thread and tile, with a byte for each of its kVecs vectors there and a bit for each column of
+// an entry.  One warp clears those of `vecs` vectors and sets its block's entries'.
+constexpr int kThreads = 256;
+constexpr int kPerSm = 4;         // blocks an SM
+constexpr int kData = kThreads - 32;
+constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
+constexpr int kTile = kData * kVecs;
+constexpr int kStages = 3;        // tiles on the way or in work
+constexpr int kRing = kStages * kTile * 16;
+constexpr int kSlice = 24576;     // vectors of a slice at most: a byte of marks each
 template <int N>
-__device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, const Own& own) {
-  for (int i = threadIdx.x & 31; i < (vecs + 3) / 4; i += 32) marks[i] = 0;
+__device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, Own& own) {
+  for (int i = threadIdx.x & 31; i < (vecs + kTile - 1) / kTile * kData; i += 32) marks[i] = 0;
   __syncwarp();
+  bool twice = false;
   for (int k = threadIdx.x & 31; k < own.n; k += 32) {
-    const int vec = own.id[k] / N - first;
-    atomicOr(&marks[vec >> 2], 1u << ((vec & 3) * 8 + own.id[k] % N));
+    const int vec = own.id[k] / N - first, tile = vec / kTile, at = vec % kTile;
+    const uint32_t bit = 1u << (at / kData * 8 + own.id[k] % N);
+    twice |= (atomicOr(&marks[tile * kData + at % kData], bit) & bit) != 0;
   }
+  twice = __any_sync(0xffffffffu, twice);
+  if ((threadIdx.x & 31) == 0) own.twice = twice;
+  __syncwarp();
 }
 
-// q's elements of the mask, or from column V on, as barred ones.
-template <typename T>
-__device__ __forceinline__ void bar(uint4& q, uint32_t mask) {
-  T* e = reinterpret_cast<T*>(&q);
-#pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i)
-    if ((mask >> i) & 1u) e[i] = static_cast<T>(-INFINITY);
-}
-template <typename T>
-__device__ __forceinline__ uint32_t beyond(int v, int V) {  // mask of the vector at column v
-  return v + Vec<T>::N <= V ? 0u : v >= V ? 0xffu : 0xffu << (V - v);
-}
 __device__ __forceinline__ void store_grad(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_grad(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Writes one vector's gradient, coef * 2^(c z - n), without the columns from V on.
+// Writes one vector's gradient, coef * 2^(c z - n), the first `columns` of it.
 template <typename T, typename G>
-__device__ __forceinline__ void write_vector(G* out, int v, int V, const uint4& q, float c, float n, float coef, bool guard) {
+__device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q, float c, float n, float coef, bool guard) {
   constexpr int N = Vec<T>::N;
   float z[N];
   widen(q, z);
@@ -384,22 +382,22 @@ __device__ __forceinline__ void write_vector(G* out, int v, int V, const uint4& 
   } else {
     for (int e = 0; e < N; ++e) z[e] = coef == 0.f ? 0.f : coef * term_guarded(z[e], c, n);
   }
-  if (v + N <= V) {
+  if (columns >= N) {
     if constexpr (sizeof(G) == 4) {
 #pragma unroll
       for (int e = 0; e < N; e += 4)
-        __stcs(reinterpret_cast<float4*>(out + v + e), make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]));
+        __stcs(reinterpret_cast<float4*>(out + e), make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]));
     } else {
       __nv_bfloat162 h[N / 2];
 #pragma unroll
       for (int e = 0; e < N; e += 2) h[e / 2] = __floats2bfloat162_rn(z[e], z[e + 1]);
-      if constexpr (N == 8) __stcs(reinterpret_cast<uint4*>(out + v), *reinterpret_cast<uint4*>(h));
-      else __stcs(reinterpret_cast<uint2*>(out + v), *reinterpret_cast<uint2*>(h));
+      if constexpr (N == 8) __stcs(reinterpret_cast<uint4*>(out), *reinterpret_cast<uint4*>(h));
+      else __stcs(reinterpret_cast<uint2*>(out), *reinterpret_cast<uint2*>(h));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      if (v + e < V) store_grad(out + v + e, z[e]);
+      if (e < columns) store_grad(out + e, z[e]);
   }
 }
 
@@ -414,13 +412,50 @@ template <int ID> __device__ __forceinline__ void bar_wait(int n) { asm volatile
 // take less than about half of it, which the launch sees to with the cluster's size.  (Holding a row in
 // registers or shared memory between the two took longer: 231 us and 346 us where this takes NNN, 1024 rows of
 // 151936 bf16.)
-constexpr int kThreads = 256;
-constexpr int kData = kThreads - 32;
-constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
-constexpr int kSlice = 24576;     // vectors of a slice at most: a byte of marks each
+// A thread's own vectors of a slice, tile after tile: asynchronous copies into its own places of shared memory keep
+// kStages - 1 tiles on the way, and no barrier is needed for them.
+struct Stream {
+  const uint4* from;  // the thread's vector of the next tile to fetch
+  uint4* ring;        // the thread's place: [kStages][kVecs][kData]
+  int left, put, get; // vectors of the slice from that tile on; places
+  __device__ __forceinline__ void fetch() {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (i * kData + (int)threadIdx.x < left)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(ring + put * kTile + i * kData)),
+                     "l"(from + i * kData)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    from += kTile;
+    left -= kTile;
+    put = put + 1 == kStages ? 0 : put + 1;
+  }
+  __device__ __forceinline__ void start(const uint4* slice, int vecs) {
+    from = slice + threadIdx.x;
+    left = vecs;
+    put = get = 0;
+#pragma unroll
+    for (int s = 0; s + 1 < kStages; ++s) fetch();
+  }
+  // The next tile; `now` vectors of the slice remain from it on.
+  template <typename T>
+  __device__ __forceinline__ void take(uint4 (&q)[kVecs], int now) {
+    fetch();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) q[i] = ring[get * kTile + i * kData];
+    if (now < kTile) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (i * kData + (int)threadIdx.x >= now) q[i] = barred_vec<T>();
+    }
+    get = get + 1 == kStages ? 0 : get + 1;
+  }
+};
 
 template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads, 4) k_distill(DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr bool kGrad = !std::is_void<G>::value;
   __shared__ struct {
@@ -430,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_distill(DistillArgs a) {
     WarpSums warps;
     Row row;
   } sh;
-  extern __shared__ uint32_t marks[];
+  extern __shared__ __align__(16) char dynamic[];
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(dynamic + kRing);
   pdl_wait();
   pdl_trigger();
   const domino_distill_t& d = a.d;
@@ -445,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_distill(DistillArgs a) {
   if (w == 0.f) {  // the whole cluster
     if constexpr (kGrad) {
       for (int vec = first + tid; vec < last; vec += kThreads)
-        write_vector<T>(out, vec * N, d.V, barred_vec<T>(), a.c, 0.f, 0.f, true);
+        write_vector<T>(out + vec * N, d.V - vec * N, barred_vec<T>(), a.c, 0.f, 0.f, true);
     }
     if (rank == 0 && tid == 0) {
       a.loss[r] = 0.f;
@@ -455,42 +491,37 @@ __global__ void __launch_bounds__(kThreads, 4) k_distill(DistillArgs a) {
   }
   cluster_arrive();  // all blocks have started before one stores into another
   if (tid < kData) {
-    constexpr int kTile = kData * kVecs;
-    auto load = [&](uint4(&q)[kVecs], int t0) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int vec = t0 + i * kData + tid;
-        const uint4* at = reinterpret_cast<const uint4*>(row) + vec;
-        q[i] = vec < last ? (kGrad ? __ldcg(at) : __ldcs(at)) : barred_vec<T>();
-      }
-    };
-    uint4 next[kVecs];
-    load(next, first);
+    const uint4* const slice = reinterpret_cast<const uint4*>(row) + first;
+    Stream in;
+    in.ring = reinterpret_cast<uint4*>(dynamic) + tid;
+    in.start(slice, last - first);
     bar_wait<1>(kThreads);  // the marks are set
+    const uint32_t* mark = marks + tid;
     ExpSum acc;
     float m = -INFINITY;
     bool guard = false;
-    for (int t0 = first; t0 < last; t0 += kTile) {
+    for (int left = last - first; left > 0; left -= kTile) {
       uint4 q[kVecs];
+      in.take<T>(q, left);
+      const uint32_t mk = *mark;
+      mark += kData;
+      if (mk) {
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) q[i] = next[i];
-      load(next, t0 + kTile);
+        for (int i = 0; i < kVecs; ++i) bar_elements<T>(q[i], (mk >> (8 * i)) & 0xffu);
+      }
+      if (left <= kTile && d.V % N != 0) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) bar_elements<T>(q[i], beyond<T>((last - left + i * kData + tid) * N, d.V));
+      }
       float tm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int vec = t0 + i * kData + tid;
-        if (vec < last) {
-          const uint32_t mask = marked(marks, vec - first) | beyond<T>(vec * N, d.V);
-          if (mask) bar<T>(q[i], mask);
-        }
-        tm = fmaxf(tm, vec_max(q[i], T()));
-      }
+      for (int i = 0; i < kVecs; ++i) tm = fmaxf(tm, vec_max(q[i], T()));
       m = fmaxf(m, tm);
       guard |= add_vectors<T>(acc, q, tm, a.c);
     }
     give_warp(sh.warps, acc, m);
     bar_arrive<2>(kThreads);  // sh.warps
-    if (kGrad) load(next, first);
+    if (kGrad) in.start(slice, last - first);
     cluster_wait();
     cluster_arrive();
     cluster_wait();
@@ -498,15 +529,19 @@ __global__ void __launch_bounds__(kThreads, 4) k_distill(DistillArgs a) {
       bar_wait<1>(kThreads);  // sh.row
       const float n = sh.row.n, coef = sh.row.coef;
       guard |= sh.row.guard != 0;
-      for (int t0 = first; t0 < last; t0 += kTile) {
+      Out* to = out + (first + tid) * N;
+      for (int left = last - first; left > 0; left -= kTile, to += kTile * N) {
         uint4 q[kVecs];
+        in.take<T>(q, left);
+        if (left > kTile) {  // whole vectors
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) q[i] = next[i];
-        load(next, t0 + kTile);
+          for (int i = 0; i < kVecs; ++i) write_vector<T>(to + i * kData * N, N, q[i], a.c, n, coef, guard);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const int vec = t0 + i * kData + tid;
-          if (vec < last) write_vector<T>(out, vec * N, d.V, q[i], a.c, n, coef, guard);
+          for (int i = 0; i < kVecs; ++i) {
+            const int vec = last - left + i * kData + tid;
+            if (vec < last) write_vector<T>(to + i * kData * N, d.V - vec * N, q[i], a.c, n, coef, guard);
+          }
         }
       }
       bar_arrive<2>(kThreads);  // the entries' columns go over the others'
@@ -596,7 +631,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
   for (int i = 0; i < kGradVecs; ++i) {
     const int vec = first + i * kGradThreads + tid;
     // the general form for NaN: this kernel has not summed the values
-    if (vec < all) write_vector<T>(out, vec * N, d.V, q[i], a.c, st.n, coef, true);
+    if (vec < all) write_vector<T>(out + vec * N, d.V - vec * N, q[i], a.c, st.n, coef, true);
   }
   __syncthreads();
   if (live && tid < own.n && firsts[tid]) store_grad(out + own.id[tid], grads[tid]);
@@ -607,7 +642,7 @@ int vectors_of(const domino_distill_t& d) { return d.dtype == DOMINO_DTYPE_F32 ?
 // Loss, and gradient where a.grad is set.
 cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
   const int vecs = vectors_of(a.d);
-  const int64_t blocks = 4 * 148;  // at a time
+  const int64_t blocks = kPerSm * 148;  // at a time
   const bool f = a.d.dtype == DOMINO_DTYPE_F32;
   int cluster = 1;
   // larger clusters: for slices that have their marks in shared memory; where few rows would leave SMs idle; and
@@ -617,11 +652,13 @@ cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
           (a.grad && std::min<int64_t>(a.d.rows, blocks / cluster) * vecs * 16 > (48 << 20) && vecs / (2 * cluster) >= 2 * kData)))
     cluster *= 2;
   a.cluster = cluster;
-  const size_t smem = ((vecs + cluster - 1) / cluster + 3) / 4 * 4;
+  const int smem = kRing + ((vecs + cluster - 1) / cluster + kTile - 1) / kTile * kTile;
   const bool g = grad_dtype == DOMINO_DTYPE_F32;
   auto kern = !a.grad ? (f ? k_distill<float, void> : k_distill<bf16, void>)
                       : f ? (g ? k_distill<float, float> : k_distill<float, bf16>)
                           : (g ? k_distill<bf16, float> : k_distill<bf16, bf16>);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   return note_launch(launch_cluster(kern, cluster, dim3((unsigned)a.d.rows * (unsigned)cluster), dim3(kThreads), smem,
                                     st, a));
 }

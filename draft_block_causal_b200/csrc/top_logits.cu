@@ -2,16 +2,16 @@
 //
 // A row is read once, by a cluster of blocks that take contiguous slices of it.  A block walks its slice in
 // tiles of kVecs 16-byte vectors a thread, the next tile's loads in flight while one is worked on: each thread
-// takes its vectors' maxima, adds the tile's exponentials, and puts the values that reach a bar, and so can
-// still be among the k largest, into a list in shared memory.  The bar comes from the threads' running maxima:
-// a value that k threads' maxima reach has k values at or above it, and not many more than k, as a thread's
-// second largest is rarely among them.  The least of the warps' j-th largest maxima, j = k / warps, is such a
-// value, and takes one barrier (an exact k-th by bisection, one barrier a probe, took four times as long).  It
-// is raised after 1, 3, 9, 27, ... tiles only, so that between them no thread waits for another; each such
-// stretch adds about 2k values.  A value in a later tile, whose column is higher, has to exceed the bar.
-// Should a stretch bring more than the list holds (ascending rows, many equal values), the exact k are selected
-// from the stretch, read again, and the list.  At the end the list is cut by the bar and goes to block 0, with
-// the sum, through distributed shared memory; block 0 cuts and ranks what it has got.
+// takes its vectors' maxima, adds the tile's exponentials, and notes the vectors whose maximum reaches a bar, so
+// that they can hold one of the k largest.  The bar comes from the threads' running maxima: a value that k
+// threads' maxima reach has k values at or above it, and not many more than k, as a thread's second largest is
+// rarely among them.  It is raised after 1, 3, 9, 27, ... tiles only, so that between them no thread waits for
+// another; each such stretch notes about 2k vectors.  A value in a later tile, whose column is higher, has to
+// exceed the bar.  At the end the noted vectors are read again, by all threads alike, and their values that reach
+// the last bar become the list of candidates: taking them as they are met cost three times the instructions,
+// since they come one lane at a time.  Should there be more than the notes or the list hold (ascending rows, many
+// equal values), the exact k are selected digit by digit from the slice.  The lists go to block 0, with the sums,
+// through distributed shared memory; block 0 cuts them by the highest bar and ranks what is left.
 #include "cluster.cuh"
 #include "launch.cuh"
 #include "vocab_rows.cuh"
@@ -26,8 +26,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;        // 16-byte vectors a thread and tile
+constexpr int kNotes = 2048;    // vectors noted
 constexpr int kList = 2048;     // candidates held
-constexpr int kTidy = 1024;     // a list longer than this is cut by the bar before the next stretch
+constexpr int kDigits = 2048;   // values of an 11-bit digit, in the place of the notes
 constexpr int kMaxCluster = 16;
 
 // Keys a block of a cluster may hand to block 0: k or more, and kList of all blocks together.
@@ -35,67 +36,60 @@ __host__ __device__ constexpr int share_bits(int cluster) { return cluster > 8 ?
 
 struct TopShared {
   alignas(16) uint64_t list[kList + 1];
-  double sum[kMaxCluster];    // block 0: every block's sum ...
-  float ref[kMaxCluster][2];  // ... its reference and maximum
-  double red_s[kWarps];
-  float red_n[kWarps], red_m[kWarps];
+  union {
+    uint32_t notes[kNotes];
+    uint32_t digits[kDigits];
+  };
+  double sum[kMaxCluster];     // block 0: every block's sum ...
+  float ref[kMaxCluster][2];   // ... its reference and maximum
+  float red_s[kWarps], red_n[kWarps], red_m[kWarps];
   uint32_t red_u[kWarps];
-  int red_i[kWarps];
-  int count;
-  int handed[kMaxCluster];    // block 0: keys of every block
-  uint32_t bars[kMaxCluster]; // block 0: every block's bar
+  int count, noted;
+  int handed[kMaxCluster];     // block 0: keys of every block
+  uint32_t bars[kMaxCluster];  // block 0: every block's bar
 };
 
 // The least float of order o or more; the orders below -FLT_MAX's are no floats'.
 __device__ __forceinline__ float floor_at(uint32_t o) { return order_value(max(o, 0x00800000u)); }
 
-// The vector at column v of a row of V with the columns from V on barred.
-template <typename T>
-__device__ __forceinline__ uint4 cut_vec(uint4 q, int v, int V) {
-  T* e = reinterpret_cast<T*>(&q);
-#pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i)
-    if (v + i >= V) e[i] = static_cast<T>(-INFINITY);
-  return q;
-}
-
-// Block 0's thread 0 gets sums over the block's threads.
+// Thread 0 gets the sum over the block's threads: in fp32 over a warp, then in 64 bits.
 __device__ __forceinline__ void join_threads(const ExpSum& a, float m, TopShared& sh, double* sum, float* ref, float* max) {
-  float n = a.n, mm = m;
+  float n = a.n;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
-    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  double s = n > -INFINITY ? (double)(a.s * ex2(a.n - n)) : 0.0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const float w = warp_sum(n > -INFINITY ? a.s * ex2(a.n - n) : 0.f);
   if ((threadIdx.x & 31) == 0) {
     sh.red_n[threadIdx.x >> 5] = n;
-    sh.red_m[threadIdx.x >> 5] = mm;
-    sh.red_s[threadIdx.x >> 5] = s;
+    sh.red_m[threadIdx.x >> 5] = m;
+    sh.red_s[threadIdx.x >> 5] = w;
   }
   __syncthreads();
   if (threadIdx.x != 0) return;
+#pragma unroll
   for (int w = 1; w < kWarps; ++w) {
     n = fmaxf(n, sh.red_n[w]);
-    mm = fmaxf(mm, sh.red_m[w]);
+    m = fmaxf(m, sh.red_m[w]);
   }
-  s = 0.0;
+  double s = 0.0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w)
-    if (sh.red_n[w] > -INFINITY) s += sh.red_s[w] * (double)ex2(sh.red_n[w] - n);
+    if (sh.red_n[w] > -INFINITY) s += (double)sh.red_s[w] * (double)ex2(sh.red_n[w] - n);
   *sum = s;
   *ref = n;
-  *max = mm;
+  *max = m;
 }
 
-constexpr int kSlots = kList / kThreads;
-
-// An order that at least k of the threads' orders o (0: none) reach.  `warps`: the warps to look at, all of whose
-// lanes take part, warps * 32 >= k.  Where one has too few values the result is 0, which all reach.
+// An order that at least k of the threads' orders o (0: none) reach, and not many more.  `warps`: the warps to look
+// at, all of whose lanes take part, warps * 32 >= k.  Where one has too few values the result may be 0, which all
+// reach.  The least of the warps' j-th largest, j = k / warps, is reached by k; three probes by bisection between
+// it and the greatest of them bring it near the k-th.
 __device__ __forceinline__ uint32_t reached_by(uint32_t o, int warps, int k, TopShared& sh) {
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t top = 0xffffffffu;
+  const uint32_t own = wid < warps ? o : 0;
+  uint32_t top = 0;
   if (wid < warps) {
     top = __reduce_max_sync(0xffffffffu, o);
     for (int j = (k + warps - 1) / warps; j > 1; --j) {
@@ -106,31 +100,21 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t o, int warps, int k, Top
   __syncthreads();  // an earlier result has been read
   if (lane == 0) sh.red_u[wid] = top;
   __syncthreads();
-  uint32_t r = sh.red_u[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) r = min(r, sh.red_u[w]);
-  return r;
+  uint32_t lo = sh.red_u[0], hi = lo;
+  for (int w = 1; w < warps; ++w) {
+    lo = min(lo, sh.red_u[w]);
+    hi = max(hi, sh.red_u[w]);
+  }
+#pragma unroll 1
+  for (int i = 0; i < 3 && hi - lo > 1; ++i) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (__syncthreads_count(own >= mid) >= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 __device__ __forceinline__ uint32_t order_bits(uint64_t key) { return (uint32_t)(key >> 32); }
-
-// Cuts the list's n keys to those of order `bar` or more; returns how many.  Ends with a barrier.
-__device__ __forceinline__ int cut_list(TopShared& sh, int n, uint32_t bar) {
-  uint64_t key[kSlots];
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const int at = threadIdx.x + i * kThreads;
-    key[i] = at < n ? sh.list[at] : 0;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) sh.count = 0;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i)
-    if (key[i] != 0 && order_bits(key[i]) >= bar) sh.list[atomicAdd(&sh.count, 1)] = key[i];
-  __syncthreads();
-  return sh.count;
-}
 
 // f(key, rank) for each of the list's n keys below rank k.
 template <typename F>
@@ -149,51 +133,80 @@ __device__ __forceinline__ void rank_list(TopShared& sh, int n, int k, F f) {
   }
 }
 
-__device__ __forceinline__ int block_count(int n, TopShared& sh) {
-  n = __reduce_add_sync(0xffffffffu, n);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh.red_i[threadIdx.x >> 5] = n;
-  __syncthreads();
-  int c = 0;
+// f(key) of every value of the vectors [first, last) of a row; whole warps call f together, with key 0 past the end.
+template <typename T, typename F>
+__device__ __forceinline__ void each_key(const T* row, int first, int last, int V, F f) {
+  for (int v0 = first; v0 < last; v0 += kThreads) {
+    const int vec = v0 + threadIdx.x;
+    float z[Vec<T>::N];
+    if (vec < last) widen(__ldcg(reinterpret_cast<const uint4*>(row) + vec), z);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) c += sh.red_i[w];
-  return c;
+    for (int e = 0; e < Vec<T>::N; ++e) {
+      const int v = vec * Vec<T>::N + e;
+      f(vec < last && v < V ? select_key(order_of(z[e]), v) : (uint64_t)0);
+    }
+  }
 }
 
-// The exact k of the `held` keys in the list and of the vectors [t0, t1) of a row, read again, into the list.
-// Returns the order of the least value kept.
+// The exact k largest of the vectors [first, last) of a row, or all if they are fewer, into the list; returns how
+// many.  The keys' bits (order, then column from the highest) are fixed 11 at a time from the top: the count of
+// the keys with each value of the digit says which the k-th has.
 template <typename T>
-__device__ __noinline__ uint32_t select_exact(const T* row, int t0, int t1, int V, int held, int k, TopShared& sh) {
-  uint64_t own[kSlots];
+__device__ __noinline__ int select_exact(const T* row, int first, int last, int V, int k, TopShared& sh) {
+  uint64_t fixed = 0;  // the k-th key's bits so far
+  int want = k;        // its place among the keys that share them
+  for (int shift = 53; shift >= -2; shift -= 11) {  // the last digit has 9 bits
+    const int bits = shift < 0 ? 9 : 11, low = shift < 0 ? 0 : shift;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) sh.digits[i] = 0;
+    __syncthreads();
+    each_key(row, first, last, V, [&](uint64_t key) {
+      const bool in = key != 0 && (low + bits == 64 || (key >> (low + bits)) == (fixed >> (low + bits)));
+      const uint32_t digit = (uint32_t)(key >> low) & ((1u << bits) - 1);
+      int same;  // whole warps of one value count once
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      __match_all_sync(0xffffffffu, in ? digit : 0xffffffffu, &same);
+      if (same) {
+        if (all && (threadIdx.x & 31) == 0) atomicAdd(&sh.digits[digit], 32u);
+      } else if (in) {
+        atomicAdd(&sh.digits[digit], 1u);
+      }
+    });
+    __syncthreads();
+    if (threadIdx.x == 0) sh.noted = sh.count = 0;  // fewer than k keys: all stay
+    // each thread has kMine digits, and the number of keys with a digit above them
+    constexpr int kMine = kDigits / kThreads;
+    int sum = 0;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const int at = threadIdx.x + i * kThreads;
-    own[i] = at < held ? sh.list[at] : 0;
-  }
-  auto each = [&](auto f) {
-    for (int vec = t0 + threadIdx.x; vec < t1; vec += kThreads) {
-      const int v = vec * Vec<T>::N;
-      for (int e = 0; e < Vec<T>::N; ++e)
-        if (v + e < V) f(select_key(order_of(to_f32(row[v + e])), v + e));
+    for (int i = 0; i < kMine; ++i) sum += (int)sh.digits[threadIdx.x * kMine + i];
+    int from_here = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_down_sync(0xffffffffu, from_here, o);
+      if ((threadIdx.x & 31) + o < 32) from_here += t;
     }
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) f(own[i]);
-  };
-  uint64_t lo = 0;  // the largest key with at least k at or above it: keys are all different
-  for (int bit = 63; bit >= 0; --bit) {
-    const uint64_t probe = lo | (1ull << bit);
-    int n = 0;
-    each([&](uint64_t key) { n += key >= probe ? 1 : 0; });
-    if (block_count(n, sh) >= k) lo = probe;
+    if ((threadIdx.x & 31) == 0) sh.red_u[threadIdx.x >> 5] = (uint32_t)from_here;
+    __syncthreads();
+    int above = from_here - sum;
+    for (int w = (threadIdx.x >> 5) + 1; w < kWarps; ++w) above += (int)sh.red_u[w];
+    if (above < want && want <= above + sum) {
+      int i = kMine - 1;
+      for (; above + (int)sh.digits[threadIdx.x * kMine + i] < want; --i) above += (int)sh.digits[threadIdx.x * kMine + i];
+      sh.noted = threadIdx.x * kMine + i;
+      sh.count = above;
+    }
+    __syncthreads();
+    fixed |= (uint64_t)sh.noted << low;
+    want -= sh.count;
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
-  each([&](uint64_t key) {
-    if (key >= lo) sh.list[atomicAdd(&sh.count, 1)] = key;
+  each_key(row, first, last, V, [&](uint64_t key) {
+    if (key != 0 && key >= fixed) sh.list[atomicAdd(&sh.count, 1)] = key;
   });
   __syncthreads();
-  return (uint32_t)(lo >> 32);
+  return sh.count;
 }
 
 template <typename T>
@@ -206,42 +219,37 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
   const int r = blockIdx.x / cluster, tid = threadIdx.x;
   const uint32_t rank = blockIdx.x % cluster;
   if ((a.scores && !(a.scores[r] > -INFINITY)) || (a.finished && a.finished[r])) return;  // the whole cluster
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) sh.count = sh.noted = 0;
   if (cluster > 1) cluster_arrive();  // block 0 has started before another stores into it
   const T* row = static_cast<const T*>(a.logits) + (size_t)r * a.ld;
   const int all = (a.V + N - 1) / N, per = (all + cluster - 1) / cluster;
   const int first = min((int)rank * per, all), last = min(first + per, all);
   constexpr int kTile = kThreads * kVecs;
-  auto load = [&](uint4(&q)[kVecs], int t0) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int vec = t0 + i * kThreads + tid;
-      q[i] = vec < last ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
-    }
-    if (a.V % N != 0 && t0 + kTile >= all) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) q[i] = cut_vec<T>(q[i], (t0 + i * kThreads + tid) * N, a.V);
-    }
-  };
   const int warps = min(last - first, kThreads) / 32;  // warps with a vector in every lane
   const bool can_bar = warps * 32 >= a.k;
   ExpSum acc;
   float m = -INFINITY;
   uint32_t bar = 0;        // an order that k values so far reach
-  float floor = -FLT_MAX;  // values from here on go to the list
+  float floor = -FLT_MAX;  // vectors with a value from here on are noted
+  const uint4* at = reinterpret_cast<const uint4*>(row) + first + tid;
   uint4 next[kVecs];
-  load(next, first);
-  int held = 0, before = 0, from = first, stop = first + kTile, stretch = 2 * kTile;
+  load_tile<T, kVecs, true>(next, at, kThreads, last - first);
+  int stop = first + kTile, stretch = 2 * kTile;
   for (int t0 = first; t0 < last;) {
     for (; t0 < min(stop, last); t0 += kTile) {
       uint4 q[kVecs];
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) q[i] = next[i];
-      load(next, t0 + kTile);
+      at += kTile;
+      load_tile<T, kVecs, true>(next, at, kThreads, last - t0 - kTile);
+      if (a.V % N != 0 && t0 + kTile >= all) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) bar_elements<T>(q[i], beyond<T>((t0 + i * kThreads + tid) * N, a.V));
+      }
       float vm[kVecs], tm = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        vm[i] = fmaxf(vec_max(q[i], T()), -INFINITY);
+        vm[i] = vec_max(q[i], T());
         tm = fmaxf(tm, vm[i]);
       }
       m = fmaxf(m, tm);
@@ -252,59 +260,64 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
       }
       if (tm >= floor) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
+        for (int i = 0; i < kVecs; ++i)
           if (vm[i] >= floor) {
-            const int v = (t0 + i * kThreads + tid) * N;
-            float z[N];
-            widen(q[i], z);
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-              if (z[e] >= floor) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList) sh.list[at] = select_key(order_of(z[e]), v + e);
-              }
+            const int to = atomicAdd(&sh.noted, 1);
+            if (to < kNotes) sh.notes[to] = t0 + i * kThreads + tid;
           }
+      }
+    }
+    if (can_bar) {
+      if (stretch > 2 * kTile) bar = max(bar, reached_by(order_of(m), warps, a.k, sh));
+      if (bar) floor = floor_at(bar + 1);
+    }
+    stop = t0 + stretch;
+    stretch *= 3;
+  }
+  __syncthreads();
+  int held = sh.noted;
+  bool exact = held > kNotes;
+  if (!exact) {
+    for (int i = tid; i < held; i += kThreads) {
+      const int vec = sh.notes[i];
+      float z[N];
+      widen(__ldcg(reinterpret_cast<const uint4*>(row) + vec), z);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const uint32_t o = order_of(z[e]);
+        if (o != 0 && o >= bar && vec * N + e < a.V) {
+          const int to = atomicAdd(&sh.count, 1);
+          if (to < kList) sh.list[to] = select_key(o, vec * N + e);
         }
       }
     }
     __syncthreads();
     held = sh.count;
-    if (held > kList) {
-      bar = max(bar, select_exact(row, from, min(t0, last), a.V, before, a.k, sh));
-      held = a.k;
-    } else if (can_bar) {
-      bar = max(bar, reached_by(order_of(m), warps, a.k, sh));
-    }
-    if (held > kTidy) held = cut_list(sh, held, bar);
-    if (bar) floor = floor_at(bar + 1);
-    before = held;
-    from = t0;
-    stop = t0 + stretch;
-    stretch *= 3;
-    __syncthreads();  // every thread has read the count before the next values come
+    exact = held > kList;
   }
+  if (exact) held = select_exact(row, first, last, a.V, a.k, sh);
   double sum = 0.0;
   float ref = -INFINITY, most = -INFINITY;
   join_threads(acc, m, sh, &sum, &ref, &most);
-  held = cut_list(sh, held, bar);
   if (cluster > 1) {
     const int bits = share_bits(cluster), share = 1 << bits;
-    if (held > share) {  // many equal values at the bar: the k largest alone
+    if (held > share) {  // the k largest alone
+      constexpr int kSlots = kList / kThreads;
       uint64_t own[kSlots];
-      int at[kSlots];
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) at[i] = kList;
+      int place[kSlots];
       int i = 0;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) place[j] = kList;
       rank_list(sh, held, a.k, [&](uint64_t key, int rk) {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
-          if (j == i) { own[j] = key; at[j] = rk; }
+          if (j == i) { own[j] = key; place[j] = rk; }
         ++i;
       });
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < kSlots; ++j)
-        if (at[j] < kList) sh.list[at[j]] = own[j];
+        if (place[j] < kList) sh.list[place[j]] = own[j];
       held = a.k;
       __syncthreads();
     }

@@ -128,6 +128,34 @@ __device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], flo
   return guard;
 }
 
+// A thread's vectors of one tile: `at` is the thread's first, the others lie `threads` apart, and `left` vectors
+// remain of the slice from the tile's first on (tid of them before the thread's).  Past the end: barred tokens.
+template <typename T, int NV, bool KEEP>
+__device__ __forceinline__ void load_tile(uint4 (&q)[NV], const uint4* at, int threads, int left) {
+  auto get = [](const uint4* p) { return KEEP ? __ldcg(p) : __ldcs(p); };
+  if (left >= NV * threads) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q[i] = get(at + i * threads);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q[i] = i * threads + (int)threadIdx.x < left ? get(at + i * threads) : barred_vec<T>();
+  }
+}
+
+// The elements of q in the mask as barred tokens.
+template <typename T>
+__device__ __forceinline__ void bar_elements(uint4& q, uint32_t mask) {
+  T* e = reinterpret_cast<T*>(&q);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N; ++i)
+    if ((mask >> i) & 1u) e[i] = static_cast<T>(-INFINITY);
+}
+// The elements, as a mask, that lie from column V on of a vector at column v.
+template <typename T>
+__device__ __forceinline__ uint32_t beyond(int v, int V) {
+  return v + Vec<T>::N <= V ? 0u : v >= V ? 0xffu : 0xffu << (V - v);
+}
+
 // Order-preserving map of a logit onto 32 bits: larger is larger, -0 equals +0; NaN and -infinity, which
 // are never selected, are 0.
 __device__ __forceinline__ uint32_t order_of(float z) {
