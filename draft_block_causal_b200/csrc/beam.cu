@@ -24,71 +24,96 @@ struct BeamArgs {
   const double* lse;     // [B * W_in]
 };
 
-__global__ void __launch_bounds__(kMergeThreads) k_beam_merge(BeamArgs a) {
+// One group by `splits` blocks: each ranks the group's candidates and takes its share of the state rows to copy.
+// A candidate's rank is what lies before it in its own beam's list, which is in order, and in each other's, found
+// by binary search.
+__global__ void __launch_bounds__(kMergeThreads) k_beam_merge(BeamArgs a, int splits) {
   __shared__ double score[DOMINO_MAX_BEAMS * DOMINO_MAX_BEAMS];
-  __shared__ int32_t token[DOMINO_MAX_BEAMS * DOMINO_MAX_BEAMS];
   __shared__ int parent_s[DOMINO_MAX_BEAMS], token_s[DOMINO_MAX_BEAMS];
+  const domino_beam_t& p = a.b;
+  const int g = blockIdx.x / splits, split = blockIdx.x % splits, tid = threadIdx.x, n = p.W_in * p.W_out;
+  constexpr int kMine = DOMINO_MAX_BEAMS * DOMINO_MAX_BEAMS / kMergeThreads;
+  int token[kMine];
   pdl_wait();
   pdl_trigger();
-  const domino_beam_t& p = a.b;
-  const int g = blockIdx.x, tid = threadIdx.x, n = p.W_in * p.W_out;
-  for (int i = tid; i < n; i += kMergeThreads) {
-    const int w = i / p.W_out, k = i % p.W_out;
+  if (tid < p.W_out) { parent_s[tid] = -1; token_s[tid] = 0; }
+#pragma unroll
+  for (int c = 0; c < kMine; ++c) {
+    const int i = tid + c * kMergeThreads;
+    if (i >= n) break;
+    const int w = i / p.W_out, k = i - w * p.W_out;
     const size_t r = (size_t)g * p.W_in + w;
     const float cum = p.scores[r];
+    const bool ended = p.finished && p.finished[r];
+    // a dead or finished beam's candidates were not written: read, and not used
+    const float z = a.values[r * p.W_out + k];
+    const int id = a.ids[r * p.W_out + k];
+    const double lse = a.lse[r];
     double sc = -INFINITY;
-    int id = 0;
     if (cum > -INFINITY) {
-      if (p.finished && p.finished[r]) {
-        if (k == 0) { sc = (double)cum; id = p.eos; }
-      } else {
-        const float z = a.values[r * p.W_out + k];
-        id = a.ids[r * p.W_out + k];
-        if (id >= 0) sc = (double)cum + ((double)big_clamp(z) - a.lse[r]);
-      }
+      if (!ended && id >= 0) sc = (double)cum + ((double)big_clamp(z) - lse);
+      if (ended && k == 0) sc = (double)cum;
     }
+    token[c] = ended ? p.eos : id;
     score[i] = sc;
-    token[i] = id;
   }
-  if (tid < p.W_out) { parent_s[tid] = -1; token_s[tid] = 0; }
   __syncthreads();
-  for (int i = tid; i < n; i += kMergeThreads) {
+#pragma unroll
+  for (int c = 0; c < kMine; ++c) {
+    const int i = tid + c * kMergeThreads;
+    if (i >= n) break;
     const double sc = score[i];
     if (!(sc > -INFINITY)) continue;
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += score[j] > sc || (score[j] == sc && j < i);
+    const int w = i / p.W_out;
+    int rank = i - w * p.W_out;
+    for (int o = 0; o < p.W_in && rank < p.W_out; ++o) {
+      if (o == w) continue;
+      int lo = 0, hi = p.W_out;  // before lo they come first, from hi on they do not
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        const double other = score[o * p.W_out + mid];
+        if (other > sc || (other == sc && o < w)) lo = mid + 1;
+        else hi = mid;
+      }
+      rank += lo;
+    }
     if (rank < p.W_out) {
-      const size_t o = (size_t)g * p.W_out + rank;
-      const int w = i / p.W_out;
       parent_s[rank] = w;
-      token_s[rank] = token[i];
-      p.scores_out[o] = (float)sc;
-      p.parents_out[o] = w;
-      p.tokens_out[o] = token[i];
-      if (p.finished_out)
-        p.finished_out[o] = (p.finished && p.finished[(size_t)g * p.W_in + w]) || token[i] == p.eos;
+      token_s[rank] = token[c];
+      if (split == 0) {
+        const size_t at = (size_t)g * p.W_out + rank;
+        p.scores_out[at] = (float)sc;
+        p.parents_out[at] = w;
+        p.tokens_out[at] = token[c];
+        if (p.finished_out)
+          p.finished_out[at] = (p.finished && p.finished[(size_t)g * p.W_in + w]) || token[c] == p.eos;
+      }
     }
   }
   __syncthreads();
-  for (int w = tid; w < p.W_out; w += kMergeThreads)
-    if (parent_s[w] < 0) {
-      const size_t o = (size_t)g * p.W_out + w;
-      p.scores_out[o] = -INFINITY;
-      p.parents_out[o] = 0;
-      p.tokens_out[o] = 0;
-      if (p.finished_out) p.finished_out[o] = 0;
+  if (split == 0 && tid < p.W_out && parent_s[tid] < 0) {
+    const size_t at = (size_t)g * p.W_out + tid;
+    p.scores_out[at] = -INFINITY;
+    p.parents_out[at] = 0;
+    p.tokens_out[at] = 0;
+    if (p.finished_out) p.finished_out[at] = 0;
+  }
+  if (p.states) {  // rows of Hs / 4 vectors, the group's as one run
+    const int per = p.Hs / 4, all = p.W_out * per;
+    const float4* from = reinterpret_cast<const float4*>(p.states) + (size_t)g * p.W_in * per;
+    float4* to = reinterpret_cast<float4*>(p.states_out) + (size_t)g * all;
+#pragma unroll 4
+    for (int i = split * kMergeThreads + tid; i < all; i += splits * kMergeThreads) {
+      const int w = i / per;
+      to[i] = __ldcs(from + (size_t)max(parent_s[w], 0) * per + (i - w * per));
     }
-  for (int w = 0; w < p.W_out; ++w) {
-    const size_t from = (size_t)g * p.W_in + max(parent_s[w], 0), to = (size_t)g * p.W_out + w;
-    if (p.states) {
-      const float4* src = reinterpret_cast<const float4*>(p.states + from * p.Hs);
-      float4* dst = reinterpret_cast<float4*>(p.states_out + to * p.Hs);
-      for (int i = tid; i < p.Hs / 4; i += kMergeThreads) dst[i] = src[i];
-    }
-    if (p.history) {
-      const int32_t* src = p.history + from * p.hist_len;
-      int32_t* dst = p.history_out + to * p.hist_len;
-      for (int i = tid; i < p.hist_len; i += kMergeThreads) dst[i] = i == p.pos ? token_s[w] : src[i];
+  }
+  if (p.history && split == splits - 1) {
+    const int all = p.W_out * p.hist_len;
+    for (int i = tid; i < all; i += kMergeThreads) {
+      const int w = i / p.hist_len, at = i - w * p.hist_len;
+      const size_t from = ((size_t)g * p.W_in + max(parent_s[w], 0)) * p.hist_len;
+      p.history_out[(size_t)g * all + i] = at == p.pos ? token_s[w] : p.history[from + at];
     }
   }
 }
@@ -171,9 +196,11 @@ extern "C" int domino_beam_select(const domino_beam_t* beam, void* workspace, si
   a.values = t.values;
   a.ids = t.ids;
   a.lse = t.lse64;
+  // blocks a group: about 4 vectors of the states a thread
+  const int splits = p.states ? std::max(1, std::min(8, p.W_out * p.Hs / (16 * kMergeThreads))) : 1;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_top_rows(t, cs);
   if (e == cudaSuccess)
-    e = note_launch(launch_pdl(k_beam_merge, dim3((unsigned)p.B), dim3(kMergeThreads), 0, cs, a));
+    e = note_launch(launch_pdl(k_beam_merge, dim3((unsigned)(p.B * splits)), dim3(kMergeThreads), 0, cs, a, splits));
   return e == cudaSuccess ? DOMINO_OK : DOMINO_ERR_CUDA;
 }

@@ -343,9 +343,7 @@ constexpr int kPerSm = 4;         // blocks an SM
 constexpr int kData = kThreads - 32;
 constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
 constexpr int kTile = kData * kVecs;
-constexpr int kStages = 3;        // tiles on the way or in work
-constexpr int kRing = kStages * kTile * 16;
-constexpr int kSlice = 24576;     // vectors of a slice at most: a byte of marks each
+constexpr int kSlice = 40960;     // vectors of a slice at most: a byte of marks each
 template <int N>
 __device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, Own& own) {
   for (int i = threadIdx.x & 31; i < (vecs + kTile - 1) / kTile * kData; i += 32) marks[i] = 0;
@@ -412,11 +410,34 @@ template <int ID> __device__ __forceinline__ void bar_wait(int n) { asm volatile
 // take less than about half of it, which the launch sees to with the cluster's size.  (Holding a row in
 // registers or shared memory between the two took longer: 231 us and 346 us where this takes NNN, 1024 rows of
 // 151936 bf16.)
-// A thread's own vectors of a slice, tile after tile: asynchronous copies into its own places of shared memory keep
-// kStages - 1 tiles on the way, and no barrier is needed for them.
-struct Stream {
+// A thread's own vectors of a slice, tile after tile.  Ahead in registers, one tile; or, for the gradient, by
+// asynchronous copies into its own places of shared memory, kStages - 1 tiles: no barrier is needed for either.
+// (Loss and gradient of 1024 rows of 151936 bf16: 136 us by registers, 127 by copies; the loss alone of 512 rows
+// fp32, whose larger slices' marks want the shared memory: 48 and 57.)
+constexpr int kStages = 3;
+constexpr int kRing = kStages * kTile * 16;
+
+struct Ahead {
+  const uint4* at;
+  uint4 next[kVecs];
+  template <typename T>
+  __device__ __forceinline__ void start(const uint4* slice, int vecs, char*) {
+    at = slice + threadIdx.x;
+    load_tile<T, kVecs, false>(next, at, kData, vecs);
+  }
+  // The next tile; `left` vectors of the slice remain from it on.
+  template <typename T>
+  __device__ __forceinline__ void take(uint4 (&q)[kVecs], int left) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) q[i] = next[i];
+    at += kTile;
+    load_tile<T, kVecs, false>(next, at, kData, left - kTile);
+  }
+};
+
+struct Copies {
   const uint4* from;  // the thread's vector of the next tile to fetch
-  uint4* ring;        // the thread's place: [kStages][kVecs][kData]
+  uint4* ring;        // the thread's places: [kStages][kVecs], kData apart
   int left, put, get; // vectors of the slice from that tile on; places
   __device__ __forceinline__ void fetch() {
 #pragma unroll
@@ -431,17 +452,18 @@ struct Stream {
     left -= kTile;
     put = put + 1 == kStages ? 0 : put + 1;
   }
-  __device__ __forceinline__ void start(const uint4* slice, int vecs) {
+  template <typename T>
+  __device__ __forceinline__ void start(const uint4* slice, int vecs, char* shared) {
+    ring = reinterpret_cast<uint4*>(shared) + threadIdx.x;
     from = slice + threadIdx.x;
     left = vecs;
     put = get = 0;
 #pragma unroll
     for (int s = 0; s + 1 < kStages; ++s) fetch();
   }
-  // The next tile; `now` vectors of the slice remain from it on.
   template <typename T>
   __device__ __forceinline__ void take(uint4 (&q)[kVecs], int now) {
-    fetch();
+    fetch();  // into the places read one tile ago
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) q[i] = ring[get * kTile + i * kData];
@@ -465,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     WarpSums warps;
     Row row;
   } sh;
-  extern __shared__ __align__(16) char dynamic[];
-  uint32_t* const marks = reinterpret_cast<uint32_t*>(dynamic + kRing);
+  extern __shared__ __align__(16) char dynamic[];  // the copies' places, then the marks
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(dynamic + (kGrad ? kRing : 0));
   pdl_wait();
   pdl_trigger();
   const domino_distill_t& d = a.d;
@@ -492,9 +514,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   cluster_arrive();  // all blocks have started before one stores into another
   if (tid < kData) {
     const uint4* const slice = reinterpret_cast<const uint4*>(row) + first;
-    Stream in;
-    in.ring = reinterpret_cast<uint4*>(dynamic) + tid;
-    in.start(slice, last - first);
+    typename std::conditional<kGrad, Copies, Ahead>::type in;
+    in.template start<T>(slice, last - first, dynamic);
     bar_wait<1>(kThreads);  // the marks are set
     const uint32_t* mark = marks + tid;
     ExpSum acc;
@@ -502,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     bool guard = false;
     for (int left = last - first; left > 0; left -= kTile) {
       uint4 q[kVecs];
-      in.take<T>(q, left);
+      in.template take<T>(q, left);
       const uint32_t mk = *mark;
       mark += kData;
       if (mk) {
@@ -521,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     }
     give_warp(sh.warps, acc, m);
     bar_arrive<2>(kThreads);  // sh.warps
-    if (kGrad) in.start(slice, last - first);
+    if (kGrad) in.template start<T>(slice, last - first, dynamic);
     cluster_wait();
     cluster_arrive();
     cluster_wait();
@@ -532,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
       Out* to = out + (first + tid) * N;
       for (int left = last - first; left > 0; left -= kTile, to += kTile * N) {
         uint4 q[kVecs];
-        in.take<T>(q, left);
+        in.template take<T>(q, left);
         if (left > kTile) {  // whole vectors
 #pragma unroll
           for (int i = 0; i < kVecs; ++i) write_vector<T>(to + i * kData * N, N, q[i], a.c, n, coef, guard);
@@ -645,14 +666,14 @@ cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
   const int64_t blocks = kPerSm * 148;  // at a time
   const bool f = a.d.dtype == DOMINO_DTYPE_F32;
   int cluster = 1;
-  // larger clusters: for slices that have their marks in shared memory; where few rows would leave SMs idle; and
-  // to keep the rows in work in about 48 MB of L2
+  // larger clusters: for slices that have their marks in shared memory; while all blocks can still run at once, so
+  // that few rows use every SM; and to keep the rows in work in about 48 MB of L2
   while (cluster < kMaxCluster &&
-         (vecs > cluster * kSlice || (a.d.rows * (int64_t)cluster < blocks && vecs / (2 * cluster) >= 2 * kData) ||
+         (vecs > cluster * kSlice || (2 * cluster * (int64_t)a.d.rows <= blocks && vecs / (2 * cluster) >= 2 * kData) ||
           (a.grad && std::min<int64_t>(a.d.rows, blocks / cluster) * vecs * 16 > (48 << 20) && vecs / (2 * cluster) >= 2 * kData)))
     cluster *= 2;
   a.cluster = cluster;
-  const int smem = kRing + ((vecs + cluster - 1) / cluster + kTile - 1) / kTile * kTile;
+  const int smem = (a.grad ? kRing : 0) + ((vecs + cluster - 1) / cluster + kTile - 1) / kTile * kTile;
   const bool g = grad_dtype == DOMINO_DTYPE_F32;
   auto kern = !a.grad ? (f ? k_distill<float, void> : k_distill<bf16, void>)
                       : f ? (g ? k_distill<float, float> : k_distill<float, bf16>)

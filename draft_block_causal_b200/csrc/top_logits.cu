@@ -374,8 +374,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
 cudaError_t launch_top_rows(const TopRows& a, cudaStream_t st) {
   const bool f = a.dtype == DOMINO_DTYPE_F32;
   const int vecs = (a.V + (f ? 3 : 7)) / (f ? 4 : 8);
+  // the largest cluster with which all blocks run at once, four an SM, and a thread has two vectors
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)a.rows * cluster < 4 * 148 && vecs / (2 * cluster) >= 2 * kThreads) cluster *= 2;
+  while (cluster < kMaxCluster && 2 * cluster * (int64_t)a.rows <= 4 * 148 && vecs / (2 * cluster) >= 2 * kThreads) cluster *= 2;
   const dim3 grid((unsigned)a.rows * (unsigned)cluster);
   const size_t smem = cluster > 1 ? ((size_t)cluster << share_bits(cluster)) * sizeof(uint64_t) : 0;
   return note_launch(f ? launch_cluster(k_top_rows<float>, cluster, grid, dim3(kThreads), smem, st, a, cluster)
