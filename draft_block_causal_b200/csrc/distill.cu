@@ -234,16 +234,65 @@ __device__ __forceinline__ Record join_records(const Record* recs, int cluster) 
   return t;
 }
 
-// What all of a block needs of a row.
-struct Row {
-  float n, coef;     // another column's gradient: coef * 2^(c z - n)
-  int live, guard;
-  double scale, P;   // w / T; the teacher's mass
-  double zn;         // p = exp(y - my) / zn
-  double all;        // S * 2^-tn: an entry's q = e * 2^(its tn - tn) / all
-  double outside;    // what of S lies outside the entries
-  float tn;
+// What a block's gradient needs of a row, in fp32.
+struct Write {
+  float n, coef;     // a column that is no entry's: coef * 2^(c z - n)
+  int guard, live;
+  float scale, P;    // w / T; the teacher's mass
+  float of_e, of_p;  // an entry's: scale * (P * of_e * e - of_p * p)
 };
+// The same and more in 64 bits, for the loss and the stats.
+struct Row {
+  int live;
+  double scale, P;
+  double zn;         // p = exp(y - my) / zn
+  double all;        // S * 2^-tn
+  double outside;    // what of S lies outside the entries
+};
+
+// One warp: Write from the blocks' records, in lanes 0 to 15.  A gradient is a difference of terms, and 2^-24 of a
+// term is a rounding of what the larger one alone would give; the loss, a difference of larger terms, goes by row_of.
+__device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int live, const Record* recs, int cluster,
+                                          float tn_own) {
+  const int lane = threadIdx.x & 31;
+  const bool in = lane < cluster;
+  const float own_n = in ? recs[lane].n : -INFINITY, own_tn = in ? recs[lane].tn : -INFINITY;
+  float n = own_n, tn = own_tn, m = in ? recs[lane].m : -INFINITY;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+    tn = fmaxf(tn, __shfl_xor_sync(0xffffffffu, tn, o));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  float s = own_n > -INFINITY ? (float)recs[lane].s * ex2(own_n - n) : 0.f;
+  float ts = own_tn > -INFINITY ? (float)recs[lane].ts * ex2(own_tn - tn) : 0.f;
+  float z = in ? (float)recs[lane].z : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    ts += __shfl_xor_sync(0xffffffffu, ts, o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  const float psum = a.d.teacher_lse ? z : 1.f;
+  const float rho = a.d.teacher_lse && s > 0.f ? fmaxf(0.f, 1.f - psum) : 0.f;
+  const float rest = s * ex2((float)(kLog2e * a.inv_t - (double)a.c) * big_clamp(m));  // c's rounding
+  Write o;
+  o.n = n;
+  o.live = live && (z > 0.f || isnan(z)) && (s > 0.f || ts > 0.f);
+  o.scale = w * (float)a.inv_t;
+  o.P = psum + rho;
+  // S at the higher of the two references
+  const bool both = s > 0.f && ts > 0.f;
+  const float gap = both ? tn - n : 0.f;
+  const float all = ts * ex2(fminf(gap, 0.f)) + rest * ex2(fminf(-gap, 0.f));
+  const float outside = rest * ex2(fminf(-gap, 0.f)) / all;
+  o.coef = o.live && s > 0.f ? o.scale * (o.P * outside - rho) / s : 0.f;
+  o.guard = o.coef == 0.f || is_extreme(m);
+  o.of_e = ts > 0.f ? ex2(tn_own - (both ? fmaxf(tn, n) : tn)) / all : 0.f;
+  o.of_p = a.d.teacher_lse ? 1.f : 1.f / z;
+  return o;
+}
+
 __device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, const Record& t) {
   Row o{};
   const double rest = t.s * rounding_of_c(t.m, a.c, a.inv_t);
@@ -253,13 +302,9 @@ __device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, c
   const double rho = a.d.teacher_lse && t.s > 0.0 ? fmax(0.0, 1.0 - psum) : 0.0;
   o.scale = (double)w * a.inv_t;
   o.P = psum + rho;
-  o.n = t.n;
-  o.tn = t.tn;
   const double gap = (double)t.n - (double)t.tn;  // infinite where one of them is
   o.outside = t.ts > 0.0 ? rest / (rest + t.ts * pow2(-gap)) : 1.0;
-  o.coef = o.live && t.s > 0.0 ? (float)(o.scale * (o.P * o.outside - rho) / t.s) : 0.f;
   o.all = t.ts + (t.s > 0.0 ? rest * pow2(gap) : 0.0);
-  o.guard = o.coef == 0.f || is_extreme(t.m);
   return o;
 }
 
@@ -281,7 +326,7 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double m
   if (a.stats) {
     Stats st;
     st.n = t.n;
-    st.rest = o.coef;
+    st.rest = t.s > 0.0 ? (float)(o.scale * (o.P * o.outside - rho) / t.s) : 0.f;
     st.l_hi = (float)L;
     st.l_lo = (float)(L - (double)st.l_hi);
     st.all = (float)(o.scale * o.P);
@@ -485,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     Own own;
     OwnSums sums;
     WarpSums warps;
-    Row row;
+    Write write;
   } sh;
   extern __shared__ __align__(16) char dynamic[];  // the copies' places, then the marks
   uint32_t* const marks = reinterpret_cast<uint32_t*>(dynamic + (kGrad ? kRing : 0));
@@ -547,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     cluster_arrive();
     cluster_wait();
     if constexpr (kGrad) {
-      bar_wait<1>(kThreads);  // sh.row
-      const float n = sh.row.n, coef = sh.row.coef;
-      guard |= sh.row.guard != 0;
+      bar_wait<1>(kThreads);  // sh.write
+      const float n = sh.write.n, coef = sh.write.coef;
+      guard |= sh.write.guard != 0;
       Out* to = out + (first + tid) * N;
       for (int left = last - first; left > 0; left -= kTile, to += kTile * N) {
         uint4 q[kVecs];
@@ -582,24 +627,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   cluster_arrive();
   cluster_wait();
   if (!kGrad && rank != 0) return;
-  const Record t = join_records(sh.recs, cluster);
-  const Row o = row_of(a, w, sh.own.live, t);
   if constexpr (kGrad) {
-    if (lane == 0) sh.row = o;
-    bar_wait<1>(kThreads);
+    const Write o = write_of(a, w, sh.own.live, sh.recs, cluster, sh.sums.tn);
+    if (lane == 0) sh.write = o;
+    bar_wait<1>(kThreads);  // sh.write
   }
-  if (rank == 0 && lane == 0) finish_row(a, r, sh.own.my, t, o);
+  if (rank == 0) {
+    const Record t = join_records(sh.recs, cluster);
+    if (lane == 0) finish_row(a, r, sh.own.my, t, row_of(a, w, sh.own.live, t));
+  }
   if constexpr (kGrad) {
     bar_wait<2>(kThreads);
-    if (sh.row.live) {
-      const Row& whole = sh.row;
-      const double to_row = pow2((double)sh.sums.tn - (double)whole.tn) / whole.all, of_teacher = 1.0 / whole.zn;
+    const Write& o = sh.write;
+    if (o.live)
       for (int k = lane; k < sh.own.n; k += 32)
         if (sh.sums.p[k] >= 0.f) {
-          const double q_v = sh.sums.e[k] > 0.f ? (double)sh.sums.e[k] * to_row : 0.0;
-          store_grad(out + sh.own.id[k], (float)(whole.scale * (whole.P * q_v - (double)sh.sums.p[k] * of_teacher)));
+          const float q_v = sh.sums.e[k] > 0.f ? sh.sums.e[k] * o.of_e : 0.f;
+          store_grad(out + sh.own.id[k], o.scale * (o.P * q_v - sh.sums.p[k] * o.of_p));
         }
-    }
   }
 }
 
@@ -743,7 +788,6 @@ extern "C" int domino_distill(const domino_distill_t* args, float* loss, float* 
     if ((rc = check_grad(*args, grad, grad_ld, grad_dtype)) != DOMINO_OK) return rc;
     const size_t n = rows_span(args->rows, args->V, grad_ld, grad_dtype);
     if (overlap(grad, n, loss, rows * 4) || overlap(grad, n, stats, rows * 32)) return DOMINO_ERR_INVALID_ARGUMENT;
-    if (!stats) return DOMINO_ERR_INVALID_ARGUMENT;
   }
   DistillArgs a = make_args(*args, status_dev);
   a.loss = loss;

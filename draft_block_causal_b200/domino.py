@@ -630,19 +630,22 @@ def _logit_rows(t, name: str):
     return shape[:-1], V, ld, code
 
 
-def _new(dims, dtype, device, stream):
-    """An uninitialised tensor whose memory belongs to the stream that the call uses it on."""
-    if stream is None:
-        return torch.empty(dims, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(dims, dtype=dtype, device=device)
+def _new(like, dims, dtype, stream):
+    """An uninitialised tensor on the device of ``like``; its memory belongs to the stream that the call uses it on."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return like.new_empty(dims, dtype=dtype)
+    if like.dtype is dtype:
+        # the cheapest ways to allocate: small calls are as long as their allocations
+        return torch.empty_like(like) if like.shape == dims and like.is_contiguous() else like.new_empty(dims)
+    return like.new_empty(dims, dtype=dtype)
 
 
-def _new_rows(lead, V: int, dtype, device, stream):
-    """An uninitialised [..., V] tensor in rows padded to a multiple of 8 values."""
+def _new_rows(like, lead, V: int, stream):
+    """An uninitialised [..., V] tensor of the type of ``like`` in rows padded to a multiple of 8 values."""
     if V % 8 == 0:
-        return _new(lead + (V,), dtype, device, stream)
-    return _new(lead + ((V + 7) // 8 * 8,), dtype, device, stream)[..., :V]
+        return _new(like, lead + (V,), like.dtype, stream)
+    return _new(like, lead + ((V + 7) // 8 * 8,), like.dtype, stream)[..., :V]
 
 
 def _raw_stream(stream, device) -> int:
@@ -670,15 +673,15 @@ def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_ou
         raise ValueError(f"k is {k}, expected 1 to {MAX_TOP}")
     sp = _raw_stream(stream, dev)
     if values_out is None:
-        values_out = _new(lead + (k,), torch.float32, dev, stream)
+        values_out = _new(logits, lead + (k,), torch.float32, stream)
     else:
         _expect(values_out, "values_out", lead + (k,), torch.float32, dev)
     if ids_out is None:
-        ids_out = _new(lead + (k,), torch.int32, dev, stream)
+        ids_out = _new(logits, lead + (k,), torch.int32, stream)
     else:
         _expect(ids_out, "ids_out", lead + (k,), torch.int32, dev)
     if lse_out is None:
-        lse_out = _new(lead, torch.float32, dev, stream)
+        lse_out = _new(values_out, lead, torch.float32, stream)
     else:
         _expect(lse_out, "lse_out", lead, torch.float32, dev)
     rc = _launch(dev, lib().domino_top_logits, logits.numel() // V, V, ld, code, logits.data_ptr(), k,
@@ -712,7 +715,7 @@ def beam_select(logits, scores, beams: int, states=None, history=None, pos: int 
     lead, V, ld, code = _logit_rows(logits, "logits")
     if len(lead) != 2:
         raise ValueError("logits must be a [B, W, V] tensor")
-    B, W = (int(x) for x in lead)
+    B, W = lead
     dev, n = logits.device, int(beams)
     if not (1 <= n <= MAX_BEAMS and W <= MAX_BEAMS):
         raise ValueError(f"{W} beams to {n}: expected 1 to {MAX_BEAMS}")
@@ -721,22 +724,23 @@ def beam_select(logits, scores, beams: int, states=None, history=None, pos: int 
     if states is not None:
         if not isinstance(states, torch.Tensor) or states.dim() != 3:
             raise ValueError("states must be a [B, W, Hs] tensor")
-        Hs = int(states.shape[2])
+        Hs = states.shape[2]
         _expect(states, "states", (B, W, Hs), torch.float32, dev)
     if history is not None:
         if not isinstance(history, torch.Tensor) or history.dim() != 3:
             raise ValueError("history must be a [B, W, hist_len] tensor")
-        hist_len = int(history.shape[2])
+        hist_len = history.shape[2]
         _expect(history, "history", (B, W, hist_len), torch.int32, dev)
     if finished is not None:
         _expect(finished, "finished", (B, W), torch.uint8, dev)
     sp = _raw_stream(stream, dev)
     if out is None:
-        three = _new((3, B, n), torch.int32, dev, stream).unbind(0)
-        out = BeamStep(three[0].view(torch.float32), three[1], three[2],
-                       None if states is None else _new((B, n, Hs), torch.float32, dev, stream),
-                       None if history is None else _new((B, n, hist_len), torch.int32, dev, stream),
-                       None if eos < 0 else _new((B, n), torch.uint8, dev, stream))
+        out_scores = _new(scores, (B, n), torch.float32, stream)
+        parents = _new(scores, (B, n), torch.int32, stream)
+        out = BeamStep(out_scores, parents, _new(parents, (B, n), torch.int32, stream),
+                       None if states is None else _new(states, (B, n, Hs), torch.float32, stream),
+                       None if history is None else _new(history, (B, n, hist_len), torch.int32, stream),
+                       None if eos < 0 else _new(scores, (B, n), torch.uint8, stream))
     else:
         _expect(out.scores, "out.scores", (B, n), torch.float32, dev)
         _expect(out.parents, "out.parents", (B, n), torch.int32, dev)
@@ -754,7 +758,7 @@ def beam_select(logits, scores, beams: int, states=None, history=None, pos: int 
         nbytes = beam_workspace_bytes(B, W, n)
         if nbytes == 0:
             raise DominoError(ERR_UNSUPPORTED, "domino_beam_workspace_bytes")
-        workspace = _new((nbytes,), torch.uint8, dev, stream)
+        workspace = _new(scores, (nbytes,), torch.uint8, stream)
     else:
         _expect_workspace(workspace, dev)
     a = BeamArgs(B, W, n, V, ld, code, int(eos), Hs, hist_len, int(pos), logits.data_ptr(), scores.data_ptr(),
@@ -797,34 +801,36 @@ def _expect_grad(grad, lead, V, dev):
 def distill(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 1.0, row_weights=None, grad_out=None,
             loss_out=None, stats_out=None, status=None, stream=None):
     """Distillation loss of every row of logits [..., V] from a teacher's top logits, and optionally its gradient in
-    the same call (``domino_distill``): returns (loss [...] fp32, grad or None, stats [..., 8] fp32).
+    the same call (``domino_distill``): returns (loss [...] fp32, grad or None, stats [..., 8] fp32 or None).
 
     top_ids [..., K] int32 (-1: no entry) and top_logits [..., K] fp32 are what ``top_logits`` gives of the teacher;
     ``teacher_lse`` [...] fp32 (its third result, at the same temperature) keeps the teacher's remaining mass as one
     class, without it the entries' probabilities are normalised.  ``row_weights`` [...] fp32 scale the rows' losses
     (0: the row is skipped).  ``grad_out``: True for a gradient in the logits' type, or a tensor (fp32 or bf16) to
     fill, which may be ``logits`` itself; it is the gradient of the sum of the losses.  ``stats`` goes to
-    ``distill_backward``."""
+    ``distill_backward``: made when no gradient is asked for, or with ``stats_out`` (True, or a tensor to fill)."""
     a, lead, V = _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_weights)
     dev = logits.device
     sp = _raw_stream(stream, dev)
-    if loss_out is None:
-        loss_out = _new(lead, torch.float32, dev, stream)
-    else:
-        _expect(loss_out, "loss_out", lead, torch.float32, dev)
-    if stats_out is None:
-        stats_out = _new(lead + (8,), torch.float32, dev, stream)
-    else:
-        _expect(stats_out, "stats_out", lead + (8,), torch.float32, dev)
-    _expect_status(status, dev)
     if grad_out is False:
         grad_out = None
+    if loss_out is None:
+        loss_out = _new(top_logits, lead, torch.float32, stream)
+    else:
+        _expect(loss_out, "loss_out", lead, torch.float32, dev)
+    if stats_out is None and grad_out is None or stats_out is True:
+        stats_out = _new(top_logits, lead + (8,), torch.float32, stream)
+    elif stats_out is False:
+        stats_out = None
+    elif stats_out is not None:
+        _expect(stats_out, "stats_out", lead + (8,), torch.float32, dev)
+    _expect_status(status, dev)
     gld = gcode = 0
     if grad_out is not None:
         if grad_out is True:
-            grad_out = _new_rows(lead, V, logits.dtype, dev, stream)
+            grad_out = _new_rows(logits, lead, V, stream)
         gld, gcode = _expect_grad(grad_out, lead, V, dev)
-    rc = _launch(dev, lib().domino_distill, ctypes.byref(a), loss_out.data_ptr(), stats_out.data_ptr(),
+    rc = _launch(dev, lib().domino_distill, ctypes.byref(a), loss_out.data_ptr(), _data(stats_out),
                  _data(grad_out), gld, gcode, _data(status), sp)
     _check(rc, "domino_distill")
     return loss_out, grad_out, stats_out
@@ -841,7 +847,7 @@ def distill_backward(logits, top_ids, top_logits, stats, grad_loss=None, teacher
         _expect(grad_loss, "grad_loss", lead, torch.float32, dev)
     sp = _raw_stream(stream, dev)
     if grad_out is None or grad_out is True:
-        grad_out = _new_rows(lead, V, logits.dtype, dev, stream)
+        grad_out = _new_rows(logits, lead, V, stream)
     gld, gcode = _expect_grad(grad_out, lead, V, dev)
     _expect_status(status, dev)
     rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(), _data(grad_loss),

@@ -331,7 +331,7 @@ DOMINO_API int domino_beam_select(const domino_beam_t* beam, void* workspace, si
  *   row_weights [rows] fp32 or NULL.
  *
  * domino_distill: loss [rows] fp32; stats [rows, 8] fp32 (16-byte aligned) for domino_distill_backward,
- *   or NULL when grad is NULL too; grad, or NULL: the gradient of the sum of the rows' losses, rows of V
+ *   or NULL; grad, or NULL: the gradient of the sum of the rows' losses, rows of V
  *   values grad_ld apart (a multiple of 8, >= V, 16-byte aligned base) in grad_dtype, rounded once;
  *   columns from V on are left as they were.
  * domino_distill_backward: the gradient of sum_r grad_loss[r] * loss[r] (grad_loss NULL: 1) from the

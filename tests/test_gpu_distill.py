@@ -181,7 +181,7 @@ def test_in_place_and_untouched_padding(V, dtype):
     z = (torch.randn(7, V, generator=g) * 2).to(DT[dtype])
     w = torch.tensor([1.0, 0.0, 2.0, 1.0, 0.5, 0.0, 1.0]).cuda()
     kw = dict(teacher_lse=lse, row_weights=w)
-    _, want, stats = domino.distill(R.padded(z), ids, val, grad_out=True, **kw)
+    _, want, stats = domino.distill(R.padded(z), ids, val, grad_out=True, stats_out=True, **kw)
     a = R.padded(z, extra=1, fill=5.0)
     domino.distill(a, ids, val, grad_out=a, **kw)
     assert torch.equal(a, want)
@@ -230,7 +230,7 @@ def test_repeats_bit_for_bit_on_streams_and_in_graphs():
     g = torch.Generator().manual_seed(81)
     ids, val, lse = teacher(40, 20000, 30, 1.0, g)
     z = (torch.randn(40, 20000, generator=g) * 2).bfloat16().cuda()
-    want = domino.distill(z, ids, val, lse, grad_out=True)
+    want = domino.distill(z, ids, val, lse, grad_out=True, stats_out=True)
     back = domino.distill_backward(z, ids, val, want[2], teacher_lse=lse)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -238,13 +238,13 @@ def test_repeats_bit_for_bit_on_streams_and_in_graphs():
     with torch.cuda.stream(s):
         torch.cuda._sleep(20_000_000)
         late.copy_(z)
-    got = domino.distill(late, ids, val, lse, grad_out=True, stream=s)
+    got = domino.distill(late, ids, val, lse, grad_out=True, stats_out=True, stream=s)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     buf = torch.zeros_like(z)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        out = domino.distill(buf, ids, val, lse, grad_out=True)
+        out = domino.distill(buf, ids, val, lse, grad_out=True, stats_out=True)
         gb = domino.distill_backward(buf, ids, val, out[2], teacher_lse=lse)
     for _ in range(2):
         buf.copy_(z)

@@ -96,7 +96,7 @@ BOTH = [dict(rows=0), dict(V=0), dict(ld=1004), dict(ld=992), dict(dtype=5), dic
         dict(grad=P + 4 * STEP), dict(grad=P + 6 * STEP)]
 
 
-@pytest.mark.parametrize("bad", BOTH + [dict(loss=None), dict(stats=None), dict(loss=P), dict(stats=P),
+@pytest.mark.parametrize("bad", BOTH + [dict(loss=None), dict(loss=P), dict(stats=P),
                                         dict(stats=P + 5 * STEP), dict(grad=P + 5 * STEP), dict(loss=P + STEP)])
 def test_distill_refusals(L, bad):
     assert distill(L, **bad) == domino.ERR_INVALID_ARGUMENT
