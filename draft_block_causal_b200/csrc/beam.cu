@@ -34,6 +34,13 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(BeamArgs a, int sp
   const int g = blockIdx.x / splits, split = blockIdx.x % splits, tid = threadIdx.x, n = p.W_in * p.W_out;
   constexpr int kMine = DOMINO_MAX_BEAMS * DOMINO_MAX_BEAMS / kMergeThreads;
   int token[kMine];
+  // the states on their way to L2 while the row scan's last blocks run
+  if (p.states) {
+    const char* from = reinterpret_cast<const char*>(p.states + (size_t)g * p.W_in * p.Hs);
+    const size_t bytes = (size_t)p.W_in * p.Hs * sizeof(float);
+    for (size_t i = (size_t)(split * kMergeThreads + tid) * 128; i < bytes; i += (size_t)splits * kMergeThreads * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+  }
   pdl_wait();
   pdl_trigger();
   if (tid < p.W_out) { parent_s[tid] = -1; token_s[tid] = 0; }
@@ -157,25 +164,26 @@ extern "C" int domino_beam_select(const domino_beam_t* beam, void* workspace, si
   const int64_t rows = (int64_t)p.B * p.W_in, outs = (int64_t)p.B * p.W_out;
   if (!rows_ok(rows, p.V, p.ld, p.dtype, p.logits)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (!p.scores || !p.scores_out || !p.parents_out || !p.tokens_out) return DOMINO_ERR_INVALID_ARGUMENT;
+  for (const void* q : {(const void*)p.scores, (const void*)p.scores_out, (const void*)p.parents_out,
+                        (const void*)p.tokens_out, (const void*)p.history, (const void*)p.history_out})
+    if (!aligned4(q)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (p.eos < -1 || p.eos >= p.V || (p.finished && (p.eos < 0 || !p.finished_out)) || (p.finished_out && p.eos < 0))
     return DOMINO_ERR_INVALID_ARGUMENT;
   if (!p.states != !p.states_out || !p.history != !p.history_out) return DOMINO_ERR_INVALID_ARGUMENT;
   if (p.states && (p.Hs < 4 || p.Hs % 4 || !a16(p.states) || !a16(p.states_out))) return DOMINO_ERR_INVALID_ARGUMENT;
   if (p.history && (p.hist_len < 1 || p.pos < 0 || p.pos >= p.hist_len)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (rows > DOMINO_MAX_ROWS || outs > DOMINO_MAX_ROWS) return DOMINO_ERR_UNSUPPORTED;
+  if ((p.states && p.Hs > (1 << 20)) || (p.history && p.hist_len > (1 << 20))) return DOMINO_ERR_UNSUPPORTED;
   const BeamLayout lay = beam_layout(p.B, p.W_in, p.W_out);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < lay.bytes)
     return DOMINO_ERR_WORKSPACE;
   // what is read while the outputs are written, by other blocks too, may not be an output
-  const struct { const void* p; size_t n; } in[] = {
-      {p.logits, rows_span(rows, p.V, p.ld, p.dtype)}, {p.scores, (size_t)rows * 4}, {p.finished, (size_t)rows},
-      {p.states, (size_t)rows * p.Hs * 4}, {p.history, (size_t)rows * p.hist_len * 4}, {workspace, lay.bytes}},
-      out[] = {{p.scores_out, (size_t)outs * 4}, {p.parents_out, (size_t)outs * 4}, {p.tokens_out, (size_t)outs * 4},
-               {p.finished_out, (size_t)outs}, {p.states_out, (size_t)outs * p.Hs * 4},
-               {p.history_out, (size_t)outs * p.hist_len * 4}};
-  for (const auto& o : out)
-    for (const auto& i : in)
-      if (overlap(o.p, o.n, i.p, i.n)) return DOMINO_ERR_INVALID_ARGUMENT;
+  const size_t outs4 = (size_t)outs * 4;
+  if (!disjoint({{p.scores_out, outs4}, {p.parents_out, outs4}, {p.tokens_out, outs4}, {p.finished_out, (size_t)outs},
+                 {p.states_out, outs4 * p.Hs}, {p.history_out, outs4 * p.hist_len}},
+                {{p.logits, rows_span(rows, p.V, p.ld, p.dtype)}, {p.scores, (size_t)rows * 4}, {p.finished, (size_t)rows},
+                 {p.states, (size_t)rows * p.Hs * 4}, {p.history, (size_t)rows * p.hist_len * 4}, {workspace, lay.bytes}}))
+    return DOMINO_ERR_INVALID_ARGUMENT;
   char* ws = static_cast<char*>(workspace);
   TopRows t{};
   t.logits = p.logits;

@@ -407,8 +407,9 @@ __device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, 
 __device__ __forceinline__ void store_grad(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_grad(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Writes one vector's gradient, coef * 2^(c z - n), the first `columns` of it.
-template <typename T, typename G>
+// Writes one vector's gradient, coef * 2^(c z - n), the first `columns` of it.  CHECK: its values may be NaN without
+// guard saying so.
+template <typename T, bool CHECK = false, typename G>
 __device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q, float c, float n, float coef, bool guard) {
   constexpr int N = Vec<T>::N;
   float z[N];
@@ -418,7 +419,8 @@ __device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
       const float2 x = fma2(make_float2(z[e], z[e + 1]), c2, n2);
-      const float2 y = mul2(make_float2(ex2(x.x), ex2(x.y)), k2);
+      const float2 t = CHECK ? make_float2(fmaxf(ex2(x.x), 0.f), fmaxf(ex2(x.y), 0.f)) : make_float2(ex2(x.x), ex2(x.y));
+      const float2 y = mul2(t, k2);
       z[e] = y.x;
       z[e + 1] = y.y;
     }
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) tm = fmaxf(tm, vec_max(q[i], T()));
       m = fmaxf(m, tm);
-      guard |= add_vectors<T>(acc, q, tm, a.c);
+      guard |= add_vectors<T>(acc, q, (left + kData - 1) / kData, tm, a.c);
     }
     give_warp(sh.warps, acc, m);
     bar_arrive<2>(kThreads);  // sh.warps
@@ -693,11 +695,11 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
   }
   __syncthreads();  // the entries' logits are read
   const float coef = live ? g * st.rest : 0.f;
+  const bool guard = coef == 0.f || is_extreme(st.n / a.c);
 #pragma unroll
   for (int i = 0; i < kGradVecs; ++i) {
     const int vec = first + i * kGradThreads + tid;
-    // the general form for NaN: this kernel has not summed the values
-    if (vec < all) write_vector<T>(out + vec * N, d.V - vec * N, q[i], a.c, st.n, coef, true);
+    if (vec < all) write_vector<T, true>(out + vec * N, d.V - vec * N, q[i], a.c, st.n, coef, guard);
   }
   __syncthreads();
   if (live && tid < own.n && firsts[tid]) store_grad(out + own.id[tid], grads[tid]);
@@ -723,7 +725,9 @@ cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
   auto kern = !a.grad ? (f ? k_distill<float, void> : k_distill<bf16, void>)
                       : f ? (g ? k_distill<float, float> : k_distill<float, bf16>)
                           : (g ? k_distill<bf16, float> : k_distill<bf16, bf16>);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the most that any call needs: host threads may be in here at once
+  constexpr int most = kRing + (kSlice + kTile - 1) / kTile * kTile;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   return note_launch(launch_cluster(kern, cluster, dim3((unsigned)a.d.rows * (unsigned)cluster), dim3(kThreads), smem,
                                     st, a));
@@ -741,23 +745,28 @@ int check_distill(const domino_distill_t* d) {
   if (!d || !rows_ok(d->rows, d->V, d->ld, d->dtype, d->logits)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (d->K < 1 || d->K > DOMINO_MAX_TOP || !temperature_ok(d->temperature)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (!d->top_ids || !d->top_logits) return DOMINO_ERR_INVALID_ARGUMENT;
+  for (const void* q : {(const void*)d->top_ids, (const void*)d->top_logits, (const void*)d->teacher_lse, (const void*)d->row_weights})
+    if (!aligned4(q)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (d->rows > DOMINO_MAX_ROWS) return DOMINO_ERR_UNSUPPORTED;
   return DOMINO_OK;
 }
 
-// Checks one output of n bytes against the inputs; `with_logits` false: the logits are checked elsewhere.
-bool clear_of_inputs(const domino_distill_t& d, const void* p, size_t n, bool with_logits) {
-  const size_t rows = (size_t)d.rows, e = rows * d.K * 4;
-  return !(with_logits && overlap(p, n, d.logits, rows_span(d.rows, d.V, d.ld, d.dtype))) &&
-         !overlap(p, n, d.top_ids, e) && !overlap(p, n, d.top_logits, e) && !overlap(p, n, d.teacher_lse, rows * 4) &&
-         !overlap(p, n, d.row_weights, rows * 4);
-}
-
-int check_grad(const domino_distill_t& d, const void* grad, int64_t grad_ld, int grad_dtype) {
-  if (!rows_ok(d.rows, d.V, grad_ld, grad_dtype, grad)) return DOMINO_ERR_INVALID_ARGUMENT;
+// The checks of a call's outputs: alignment, and that no two of them, nor one and an input, share memory -- but
+// for a gradient in the place of the logits.  grad_loss: another input, or null.
+int check_outputs(const domino_distill_t& d, const float* loss, const float* stats, bool stats_out, const float* grad_loss,
+                  const void* grad, int64_t grad_ld, int grad_dtype) {
+  if (!aligned4(loss) || !aligned4(grad_loss) || (reinterpret_cast<uintptr_t>(stats) & 15u)) return DOMINO_ERR_INVALID_ARGUMENT;
+  if (grad && !rows_ok(d.rows, d.V, grad_ld, grad_dtype, grad)) return DOMINO_ERR_INVALID_ARGUMENT;
+  const size_t rows = (size_t)d.rows, e = rows * d.K * 4, in_bytes = rows_span(d.rows, d.V, d.ld, d.dtype);
+  const size_t grad_bytes = grad ? rows_span(d.rows, d.V, grad_ld, grad_dtype) : 0;
   const bool in_place = grad == d.logits && grad_ld == d.ld && grad_dtype == d.dtype;
-  return clear_of_inputs(d, grad, rows_span(d.rows, d.V, grad_ld, grad_dtype), !in_place) ? DOMINO_OK
-                                                                                          : DOMINO_ERR_INVALID_ARGUMENT;
+  const Range ids{d.top_ids, e}, tops{d.top_logits, e}, lse{d.teacher_lse, rows * 4}, w{d.row_weights, rows * 4},
+      given{stats_out ? nullptr : stats, rows * 32}, up{grad_loss, rows * 4};
+  if (!disjoint({{loss, rows * 4}, {stats_out ? stats : nullptr, rows * 32}, {grad, grad_bytes}}, {ids, tops, lse, w, given, up}) ||
+      !disjoint({{loss, rows * 4}, {stats_out ? stats : nullptr, rows * 32}, {in_place ? nullptr : grad, grad_bytes}},
+                {{d.logits, in_bytes}}))
+    return DOMINO_ERR_INVALID_ARGUMENT;
+  return DOMINO_OK;
 }
 
 DistillArgs make_args(const domino_distill_t& d, int32_t* status) {
@@ -779,16 +788,8 @@ extern "C" int domino_distill(const domino_distill_t* args, float* loss, float* 
                               int32_t grad_dtype, int32_t* status_dev, domino_stream_t stream) {
   int rc = check_distill(args);
   if (rc != DOMINO_OK) return rc;
-  if (!loss || (stats && (reinterpret_cast<uintptr_t>(stats) & 15u))) return DOMINO_ERR_INVALID_ARGUMENT;
-  const size_t rows = (size_t)args->rows;
-  if (!clear_of_inputs(*args, loss, rows * 4, true) || !clear_of_inputs(*args, stats, rows * 32, true) ||
-      overlap(loss, rows * 4, stats, rows * 32))
-    return DOMINO_ERR_INVALID_ARGUMENT;
-  if (grad) {
-    if ((rc = check_grad(*args, grad, grad_ld, grad_dtype)) != DOMINO_OK) return rc;
-    const size_t n = rows_span(args->rows, args->V, grad_ld, grad_dtype);
-    if (overlap(grad, n, loss, rows * 4) || overlap(grad, n, stats, rows * 32)) return DOMINO_ERR_INVALID_ARGUMENT;
-  }
+  if (!loss || !aligned4(status_dev)) return DOMINO_ERR_INVALID_ARGUMENT;
+  if ((rc = check_outputs(*args, loss, stats, true, nullptr, grad, grad_ld, grad_dtype)) != DOMINO_OK) return rc;
   DistillArgs a = make_args(*args, status_dev);
   a.loss = loss;
   a.stats = reinterpret_cast<float4*>(stats);
@@ -804,10 +805,8 @@ extern "C" int domino_distill_backward(const domino_distill_t* args, const float
                                        domino_stream_t stream) {
   int rc = check_distill(args);
   if (rc != DOMINO_OK) return rc;
-  if (!stats || (reinterpret_cast<uintptr_t>(stats) & 15u)) return DOMINO_ERR_INVALID_ARGUMENT;
-  if ((rc = check_grad(*args, grad, grad_ld, grad_dtype)) != DOMINO_OK) return rc;
-  const size_t rows = (size_t)args->rows, n = rows_span(args->rows, args->V, grad_ld, grad_dtype);
-  if (overlap(grad, n, stats, rows * 32) || overlap(grad, n, grad_loss, rows * 4)) return DOMINO_ERR_INVALID_ARGUMENT;
+  if (!stats || !grad || !aligned4(status_dev)) return DOMINO_ERR_INVALID_ARGUMENT;
+  if ((rc = check_outputs(*args, nullptr, stats, false, grad_loss, grad, grad_ld, grad_dtype)) != DOMINO_OK) return rc;
   DistillArgs a = make_args(*args, status_dev);
   a.stats = reinterpret_cast<float4*>(const_cast<float*>(stats));
   a.grad_loss = grad_loss;

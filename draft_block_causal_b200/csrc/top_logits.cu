@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
         tm = fmaxf(tm, vm[i]);
       }
       m = fmaxf(m, tm);
-      add_vectors<T>(acc, q, tm, a.c);
+      add_vectors<T>(acc, q, (last - t0 + kThreads - 1) / kThreads, tm, a.c);
       if (bar == 0 && can_bar) {  // no bar yet: this tile's columns may be the lowest that reach it
         bar = reached_by(order_of(m), warps, a.k, sh);
         floor = floor_at(bar);
@@ -392,8 +392,9 @@ extern "C" int domino_top_logits(int32_t rows, int32_t V, int64_t ld, int32_t dt
   if (!rows_ok(rows, V, ld, dtype, logits) || !values || !ids) return DOMINO_ERR_INVALID_ARGUMENT;
   if (k < 1 || k > DOMINO_MAX_TOP || !temperature_ok(temperature)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (rows > DOMINO_MAX_ROWS) return DOMINO_ERR_UNSUPPORTED;
-  const size_t in = rows_span(rows, V, ld, dtype), out = (size_t)rows * k * 4;
-  if (overlap(logits, in, values, out) || overlap(logits, in, ids, out) || overlap(logits, in, lse, (size_t)rows * 4))
+  if (!aligned4(values) || !aligned4(ids) || !aligned4(lse)) return DOMINO_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)rows * k * 4;
+  if (!disjoint({{values, n}, {ids, n}, {lse, (size_t)rows * 4}}, {{logits, rows_span(rows, V, ld, dtype)}}))
     return DOMINO_ERR_INVALID_ARGUMENT;
   TopRows a{};
   a.logits = logits;

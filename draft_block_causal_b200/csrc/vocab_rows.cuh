@@ -93,17 +93,18 @@ __device__ __forceinline__ void raise(ExpSum& a, float n) {
   a.n = n;
 }
 
-// Adds vectors of maximum m (NaN aside) to a thread's sum; true where their terms need a guard.  The reference is
+// Adds the first `some` of the vectors, of maximum m (NaN aside), to a thread's sum; true where their terms need a guard.  The reference is
 // raised only when a term would exceed 2^kSlack of it, so that it hardly ever is after the first vectors.
 constexpr float kSlack = 40.f;
 template <typename T, int NV>
-__device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], float m, float c) {
+__device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], int some, float m, float c) {
   if (!(m > -INFINITY)) return false;
   if (fmaf(big_clamp(m), c, -a.n) > kSlack) raise(a, reference_of(m, c));
   float2 s = make_float2(0.f, 0.f);
   const float2 c2 = make_float2(c, c), n2 = make_float2(-a.n, -a.n);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
+    if (i >= some) break;
     float z[Vec<T>::N];
     widen(q[i], z);
 #pragma unroll

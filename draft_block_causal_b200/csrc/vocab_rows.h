@@ -23,8 +23,26 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && x < y + nb && y < x + na;
 }
 
-// The k largest logits and the log-sum-exp of every row (top_logits.cu).  live: rows to scan, or null;
-// row r is skipped, its outputs left alone, when scores[r] is not above -infinity or finished[r] != 0.
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Outputs of a call against its inputs and against each other (null: not there).
+struct Range {
+  const void* p;
+  size_t n;
+};
+template <int OUT, int IN>
+bool disjoint(const Range (&out)[OUT], const Range (&in)[IN]) {
+  for (int i = 0; i < OUT; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i].p, out[i].n, r.p, r.n)) return false;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return false;
+  }
+  return true;
+}
+
+// The k largest logits and the log-sum-exp of every row (top_logits.cu).  Row r is skipped, its outputs left
+// alone, when scores (or null) has nothing above -infinity for it or finished (or null) is not 0.
 struct TopRows {
   const void* logits;
   int64_t ld;

@@ -867,9 +867,18 @@ class _DistillLoss(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
+        # the arguments were checked in forward; what is saved may come back elsewhere, but alike
         logits, top_ids, top_logits, teacher_lse, row_weights, stats = ctx.saved_tensors
-        grad = distill_backward(logits, top_ids, top_logits, stats, grad_loss.contiguous(), teacher_lse,
-                                ctx.temperature, row_weights)
+        lead, V, ld, code = _logit_rows(logits, "logits")
+        dev = logits.device
+        if not grad_loss.is_contiguous():
+            grad_loss = grad_loss.contiguous()
+        grad = _new_rows(logits, lead, V, None)
+        a = DistillArgs(stats.numel() // 8, V, ld, code, top_ids.shape[-1], logits.data_ptr(), top_ids.data_ptr(),
+                        top_logits.data_ptr(), _data(teacher_lse), _data(row_weights), ctx.temperature)
+        rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(), grad_loss.data_ptr(),
+                     grad.data_ptr(), (V + 7) // 8 * 8, code, None, _raw_stream(None, dev))
+        _check(rc, "domino_distill_backward")
         return grad, None, None, None, None, None, None
 
 

@@ -70,7 +70,7 @@ extern "C" {
 /* Device status codes written to *status_dev. */
 #define DOMINO_STATUS_OK 0
 #define DOMINO_STATUS_DEVICE_TIMEOUT 1 /* a bounded device-wide wait gave up; outputs invalid */
-#define DOMINO_STATUS_BAD_TOKEN 2      /* a teacher-forcing token was outside [0, V)          */
+#define DOMINO_STATUS_BAD_TOKEN 2      /* a token given to the call was outside [0, V)         */
 
 /* cudaStream_t, kept opaque so this header needs no CUDA include. */
 typedef void* domino_stream_t;
@@ -248,7 +248,7 @@ DOMINO_API int domino_accept_sample(int32_t B, int32_t L, int32_t V, const int32
  *
  * They read logits as `rows` rows of V values, fp32 or bf16 (`dtype`), `ld` values apart: V may be
  * any number from 1 to DOMINO_MAX_V and need not be a multiple of 8, but ld must be (ld >= V), the
- * base must be 16-byte aligned, and V rounded up to a multiple of 8 values must be readable in every
+ * base must be 16-byte aligned (the other arrays to their elements), and V rounded up to a multiple of 8 values must be readable in every
  * row (what lies there is ignored, and never written).  rows <= DOMINO_MAX_ROWS.
  *
  * A logit of -infinity is a barred token: it has no mass and is never selected.  NaN counts as
@@ -288,7 +288,8 @@ DOMINO_API int domino_top_logits(int32_t rows, int32_t V, int64_t ld, int32_t dt
  *   hist_len] = the parent's history with the token at `pos`.  states_out and history_out go with their
  *   inputs.  Where a group has fewer than W_out continuations the remaining beams are dead: score
  *   -infinity, parent 0, token 0, finished 0.
- * No output may overlap an input (DOMINO_ERR_INVALID_ARGUMENT).  1 <= W_in, W_out <= DOMINO_MAX_BEAMS.
+ * No output may overlap an input or another (DOMINO_ERR_INVALID_ARGUMENT).  1 <= W_in, W_out <=
+ * DOMINO_MAX_BEAMS; Hs and hist_len up to 2^20 (else DOMINO_ERR_UNSUPPORTED).
  * Needs domino_beam_workspace_bytes(B, W_in, W_out) bytes of workspace (256-byte aligned). */
 typedef struct {
   int32_t B, W_in, W_out, V;
@@ -337,8 +338,8 @@ DOMINO_API int domino_beam_select(const domino_beam_t* beam, void* workspace, si
  * domino_distill_backward: the gradient of sum_r grad_loss[r] * loss[r] (grad_loss NULL: 1) from the
  *   same arguments and the stats that domino_distill wrote for them; a row whose grad_loss is 0 is not
  *   read and its gradient is 0.
- * grad may be the logits themselves (same ld and dtype); no other overlap of outputs with inputs is
- * allowed (DOMINO_ERR_INVALID_ARGUMENT). */
+ * grad may be the logits themselves (same ld and dtype); outputs may not overlap inputs or each other
+ * otherwise (DOMINO_ERR_INVALID_ARGUMENT). */
 typedef struct {
   int32_t rows, V;
   int64_t ld;

@@ -111,8 +111,9 @@ def test_temperatures(T, tail):
 
 @pytest.mark.parametrize("tail", [False, True], ids=["entries", "rest"])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-def test_ignored_rows_barred_tokens_and_unusual_entries(dtype, tail):
-    rows, V, K = 16, 2003, 10
+@pytest.mark.parametrize("V", [2003, 70003])
+def test_ignored_rows_barred_tokens_and_unusual_entries(V, dtype, tail):
+    rows, K = 16, 10
     g = torch.Generator().manual_seed(21)
     ids, val, lse = teacher(rows, V, K, 1.0, g)
     z = torch.randn(rows, V, generator=g) * 2
@@ -276,3 +277,50 @@ def test_a_graph_captured_training_step_replays():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(x.grad, want)
+
+
+def test_offsets_beyond_32_bits():
+    rows, V = 16400, 131072  # 2^31 values and more, 4.3 GB, the gradient in their place
+    z = torch.empty(rows, V, dtype=torch.bfloat16, device="cuda").normal_()
+    last = z[-3:].clone()
+    g = torch.Generator().manual_seed(3)
+    ids, val, lse = teacher(4, V, 6, 1.0, g)
+    ids, val, lse = (t.repeat(rows // 4, *([1] * (t.dim() - 1))).contiguous() for t in (ids, val, lse))
+    loss, _, stats = domino.distill(z, ids, val, lse)
+    back = domino.distill_backward(last, ids[-3:].contiguous(), val[-3:].contiguous(), stats[-3:].contiguous(),
+                                   teacher_lse=lse[-3:].contiguous())
+    fused, _, _ = domino.distill(z, ids, val, lse, grad_out=z)
+    torch.cuda.synchronize()
+    want, gwant, scale = expected(last, ids[-3:], val[-3:], lse[-3:], 1.0, None)
+    for l in (loss, fused):
+        check_loss(l[-3:], want, V, None)
+    for x in (back, z[-3:]):
+        check_grad(x, gwant, scale, None, last, 1.0)
+
+
+def test_autograd_contract():
+    g = torch.Generator().manual_seed(101)
+    ids, val, lse = teacher(6, 1200, 5, 1.0, g)
+    x = torch.randn(6, 1200, generator=g).cuda().requires_grad_()
+    loss = domino.distill_loss(x * 1.0, ids, val, lse)      # a non-leaf
+    (g1,) = torch.autograd.grad(loss.sum(), x, retain_graph=True)
+    (g2,) = torch.autograd.grad(loss.sum(), x)               # twice from one graph
+    assert torch.equal(g1, g2)
+    with torch.no_grad():
+        assert not domino.distill_loss(x, ids, val, lse).requires_grad
+    # second derivatives are refused, and so is a backward pass over logits that were changed
+    loss = domino.distill_loss(x, ids, val, lse)
+    (g3,) = torch.autograd.grad(loss.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g3.sum(), x)
+    y = x.detach().clone().requires_grad_()
+    z = y * 1.0
+    loss = domino.distill_loss(z, ids, val, lse)
+    z.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    # saved tensors that come back from the host
+    with torch.autograd.graph.save_on_cpu():
+        loss = domino.distill_loss(x, ids, val, lse)
+    (g4,) = torch.autograd.grad(loss.sum(), x)
+    assert torch.equal(g4, g1)

@@ -66,8 +66,8 @@ def test_orders_and_ties(kind, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-def test_barred_and_unusual_rows(dtype):
-    V = 3001
+@pytest.mark.parametrize("V", [3001, 70001])
+def test_barred_and_unusual_rows(V, dtype):
     g = torch.Generator().manual_seed(11)
     z = torch.randn(12, V, generator=g) * 2
     low = torch.finfo(DT[dtype]).min
@@ -133,3 +133,42 @@ def test_on_another_stream_and_in_a_graph():
         ref = domino.top_logits(x, 12)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_offsets_beyond_32_bits():
+    rows, V = 16400, 131072  # 2^31 values and more, 4.3 GB
+    z = torch.empty(rows, V, dtype=torch.bfloat16, device="cuda").normal_()
+    values, ids, lse = domino.top_logits(z, 5)
+    torch.cuda.synchronize()
+    last = z[-3:].double().cpu().numpy()
+    want_v, want_i = R.top(last, 5)
+    np.testing.assert_array_equal(ids[-3:].cpu().numpy(), want_i)
+    np.testing.assert_array_equal(values[-3:].double().cpu().numpy(), want_v)
+    want = R.lse_rows(last, 1.0)
+    assert (np.abs(lse[-3:].double().cpu().numpy() - want) <= R.sum_tol(V) + 2.0 ** -23 * np.abs(want)).all()
+
+
+def test_two_calls_at_once():
+    """Calls from two host threads on two streams, of different sizes, give what they give alone."""
+    import threading
+    jobs = []
+    for i, (rows, V, k) in enumerate(((3, 151936, 20), (200, 9000, 64))):
+        z = torch.randn(rows, V, generator=torch.Generator().manual_seed(i)).cuda()
+        jobs.append((z, k, torch.cuda.Stream(), domino.top_logits(z, k)))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        z, k, s, _ = jobs[i]
+        for _ in range(40):
+            got[i].append(domino.top_logits(z, k, stream=s))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i, (_, _, _, want) in enumerate(jobs):
+        assert len(got[i]) == 40
+        assert all(torch.equal(a, b) for out in got[i] for a, b in zip(out, want))

@@ -30,7 +30,9 @@ def top(L, **kw):
                                  dict(ld=1001), dict(ld=992), dict(dtype=2), dict(dtype=-1), dict(logits=None),
                                  dict(logits=P + 8), dict(k=0), dict(k=129), dict(T=0.0), dict(T=-1.0), dict(T=1e-4),
                                  dict(T=1025.0), dict(T=float("nan")), dict(T=float("inf")), dict(values=None),
-                                 dict(ids=None), dict(values=P + 4 * 3999), dict(ids=P), dict(lse=P + 4)])
+                                 dict(ids=None), dict(values=P + 4 * 3999), dict(ids=P), dict(lse=P + 4), dict(values=P + STEP + 2),
+                                 dict(ids=P + 2 * STEP + 1), dict(lse=P + 3 * STEP + 3), dict(lse=P + STEP + 16),
+                                 dict(ids=P + STEP + 4)])
 def test_top_logits_refusals(L, bad):
     assert top(L, **bad) == domino.ERR_INVALID_ARGUMENT
 
@@ -58,7 +60,9 @@ def beam(L, ws=P + 20 * STEP, ws_bytes=1 << 40, **kw):
                                  dict(Hs=62), dict(Hs=0), dict(states=P + 2 * STEP + 4), dict(hist_len=0), dict(pos=-1),
                                  dict(pos=16), dict(states_out=P + 2 * STEP), dict(history_out=P + 3 * STEP + 64),
                                  dict(scores_out=P + STEP), dict(tokens_out=P + 3 * STEP),
-                                 dict(parents_out=P + 20 * STEP)])
+                                 dict(parents_out=P + 20 * STEP), dict(scores=P + STEP + 2),
+                                 dict(tokens_out=P + 6 * STEP + 1), dict(history=P + 3 * STEP + 2),
+                                 dict(tokens_out=P + 5 * STEP), dict(scores_out=P + 7 * STEP + 4)])
 def test_beam_select_refusals(L, bad):
     assert beam(L, **bad) == domino.ERR_INVALID_ARGUMENT
 
@@ -71,6 +75,8 @@ def test_beam_select_workspace_and_limits(L):
     assert L.domino_beam_select(None, P, n, None) == domino.ERR_INVALID_ARGUMENT
     for bad in ((0, 3, 4), (2, 0, 4), (2, 3, 33), (1 << 22, 3, 4)):
         assert L.domino_beam_workspace_bytes(*bad) == 0
+    assert beam(L, Hs=(1 << 20) + 4) == domino.ERR_UNSUPPORTED
+    assert beam(L, hist_len=(1 << 20) + 1) == domino.ERR_UNSUPPORTED
     assert beam(L, B=1 << 21, V=8, ld=8, states=None, states_out=None, history=None,
                 history_out=None) == domino.ERR_UNSUPPORTED
 
@@ -93,16 +99,18 @@ BOTH = [dict(rows=0), dict(V=0), dict(ld=1004), dict(ld=992), dict(dtype=5), dic
         dict(temperature=float("nan")), dict(temperature=2000.0), dict(stats=P + 6 * STEP + 8), dict(grad_ld=996),
         dict(grad_ld=0), dict(grad_dtype=2), dict(grad=P + 7 * STEP + 2), dict(grad=P + 16), dict(grad=P, grad_dtype=0),
         dict(grad=P, grad_ld=1008), dict(grad=P + STEP), dict(grad=P + 2 * STEP), dict(grad=P + 3 * STEP),
-        dict(grad=P + 4 * STEP), dict(grad=P + 6 * STEP)]
+        dict(grad=P + 4 * STEP), dict(grad=P + 6 * STEP), dict(top_ids=P + STEP + 2), dict(top_logits=P + 2 * STEP + 1),
+        dict(teacher_lse=P + 3 * STEP + 3), dict(row_weights=P + 4 * STEP + 2)]
 
 
 @pytest.mark.parametrize("bad", BOTH + [dict(loss=None), dict(loss=P), dict(stats=P),
-                                        dict(stats=P + 5 * STEP), dict(grad=P + 5 * STEP), dict(loss=P + STEP)])
+                                        dict(stats=P + 5 * STEP), dict(grad=P + 5 * STEP), dict(loss=P + STEP), dict(loss=P + 5 * STEP + 2)])
 def test_distill_refusals(L, bad):
     assert distill(L, **bad) == domino.ERR_INVALID_ARGUMENT
 
 
-@pytest.mark.parametrize("bad", BOTH + [dict(stats=None), dict(grad=None), dict(grad=P + 8 * STEP)])
+@pytest.mark.parametrize("bad", BOTH + [dict(stats=None), dict(grad=None), dict(grad=P + 8 * STEP),
+                                        dict(grad_loss=P + 8 * STEP + 1)])
 def test_distill_backward_refusals(L, bad):
     assert distill(L, "backward", **bad) == domino.ERR_INVALID_ARGUMENT
 
