@@ -91,8 +91,10 @@ __device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, in
   const int lane = threadIdx.x & 31;
   int32_t id[kEach];
   float t[kEach], most = -INFINITY;
+  const float lse = d.teacher_lse ? d.teacher_lse[r] : 0.f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= d.K) break;
     const int k = 32 * i + lane;
     id[i] = -1;
     t[i] = -INFINITY;
@@ -104,6 +106,7 @@ __device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, in
   int n = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= d.K) break;
     if (id[i] < 0 || id[i] >= d.V) {
       if (id[i] != -1 && report && a.status) set_status(a.status, DOMINO_STATUS_BAD_TOKEN);
       id[i] = -1;
@@ -124,7 +127,6 @@ __device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, in
   if (lane == 0) {
     own.n = n;
     if (d.teacher_lse) {
-      const float lse = d.teacher_lse[r];
       own.live = fabsf(lse) < INFINITY;
       own.my = own.live ? (double)lse : 0.0;
     } else {
@@ -151,40 +153,43 @@ __device__ __forceinline__ double exp2_near(double t) {
 template <typename T>
 __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, const T* row, OwnSums& sums) {
   const int lane = threadIdx.x & 31, n = own.n;
-  double ts = 0.0, zs = 0.0, as = 0.0;
-  float tn = -INFINITY;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    const int k = k0 + lane;
-    const float z = k < n ? to_f32(row[own.id[k]]) : -INFINITY;
-    const double x = z > -INFINITY ? (double)big_clamp(z) * a.inv_t : -INFINITY;
-    float most = z > -INFINITY ? (float)ceil(x * kLog2e) : -INFINITY;
+  float z[kEach], most = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (most > tn) {  // entries before these are taken to the new reference
-      if (tn > -INFINITY) {
-        const double by = pow2((double)tn - (double)most);
-        ts *= by;
-        for (int j = lane; j < k0; j += 32) sums.e[j] *= (float)by;
-      }
-      tn = most;
-    }
-    if (k >= n) continue;
-    const int id = own.id[k];
-    const double y = own.y[k], pt = y > -INFINITY ? exp2_near((y - own.my) * kLog2e) : 0.0;
+  for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= n) break;
+    z[i] = 32 * i + lane < n ? to_f32(row[own.id[32 * i + lane]]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= n) break;
+    most = fmaxf(most, z[i]);  // NaN aside
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  const double to2 = a.inv_t * kLog2e, tn = most > -INFINITY ? ceil((double)big_clamp(most) * to2) : 0.0;
+  double ts = 0.0, zs = 0.0, as = 0.0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= n) break;
+    const int k = 32 * i + lane;
+    if (k >= n) break;
+    const double y = own.y[k], x = (double)big_clamp(z[i]);
+    const double pt = y > -INFINITY ? exp2_near((y - own.my) * kLog2e) : 0.0;
+    const double e = z[i] > -INFINITY ? exp2_near(x * to2 - tn) : 0.0;
     double p = pt;
-    const double e = x > -INFINITY ? exp2_near(x * kLog2e - (double)tn) : 0.0;
     bool first = true;
-    if (own.twice)
+    if (own.twice) {
       for (int j = 0; j < n; ++j)
-        if (own.id[j] == id && j != k) {
+        if (own.id[j] == own.id[k] && j != k) {
           first &= j > k;
           if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - own.my) * kLog2e);
         }
+    }
     sums.e[k] = (float)e;
     sums.p[k] = first ? (float)p : -1.f;
     if (first) ts += e;
     zs += pt;
-    if (pt > 0.0) as += pt * (y - x);
+    if (pt > 0.0) as += z[i] > -INFINITY ? pt * (y - x * a.inv_t) : INFINITY;
   }
   __syncwarp();
 #pragma unroll
@@ -194,7 +199,7 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, co
     as += __shfl_xor_sync(0xffffffffu, as, o);
   }
   if (lane == 0) {
-    sums.tn = tn;
+    sums.tn = most > -INFINITY ? (float)tn : -INFINITY;
     sums.ts = ts;
     sums.z = zs;
     sums.a = as;
@@ -212,6 +217,7 @@ __device__ __forceinline__ double rounding_of_c(float m, float c, double inv_t) 
 __device__ __forceinline__ Record join_records(const Record* recs, int cluster) {
   const int lane = threadIdx.x & 31;
   Record t{0.0, 0.0, 0.0, 0.0, -INFINITY, -INFINITY, -INFINITY};
+  if (cluster == 1) return recs[0];
   if (lane < cluster) t = recs[lane];
   float n = t.n, tn = t.tn;
 #pragma unroll
@@ -659,8 +665,7 @@ template <typename T, typename G>
 __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ Own own;
-  __shared__ float grads[kMaxK];  // an entry's gradient, where it is the first of its token's
-  __shared__ bool firsts[kMaxK];
+  __shared__ uint32_t bits[kGradThreads * kGradVecs * N / 32];  // the chunk's columns that are entries'
   pdl_wait();
   pdl_trigger();
   const domino_distill_t& d = a.d;
@@ -677,20 +682,33 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
     const int vec = first + i * kGradThreads + tid;
     q[i] = live && vec < all ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
   }
-  if (tid < 32 && live) {
-    find_own(a, r, first * N, min(first + kGradThreads * kGradVecs, all) * N, own, false);
-    const double lp = (double)st.lp_hi + (double)st.lp_lo, L = (double)st.l_hi + (double)st.l_lo;
-    for (int k = tid; k < own.n; k += 32) {
-      double p = 0.0;
-      firsts[k] = true;
-      for (int j = 0; j < own.n; ++j)
-        if (own.id[j] == own.id[k]) {
-          if (own.y[j] > -INFINITY) p += exp(own.y[j] - lp);
-          if (j < k) firsts[k] = false;
-        }
-      const float z = to_f32(row[own.id[k]]);
-      const double q_v = z > -INFINITY ? exp((double)big_clamp(z) * a.inv_t - L) : 0.0;
-      grads[k] = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
+  float own_grad = 0.f;
+  int own_at = -1;  // the column of the thread's entry, where it is the first of its token's
+  if (live) {
+    for (int i = tid; i < kGradThreads * kGradVecs * N / 32; i += kGradThreads) bits[i] = 0;
+    if (tid < 32) find_own(a, r, first * N, min(first + kGradThreads * kGradVecs, all) * N, own, false);
+    __syncthreads();
+    bool again = false;
+    if (tid < own.n) {
+      own_at = own.id[tid];
+      const int at = own_at - first * N;
+      const uint32_t bit = 1u << (at & 31);
+      again = (atomicOr(&bits[at >> 5], bit) & bit) != 0;
+    }
+    const bool twice = __syncthreads_or(again);
+    if (own_at >= 0) {
+      const double lp = (double)st.lp_hi + (double)st.lp_lo, L = (double)st.l_hi + (double)st.l_lo;
+      const float z = to_f32(row[own_at]);
+      double p = own.y[tid] > -INFINITY ? exp2_near((own.y[tid] - lp) * kLog2e) : 0.0;
+      const double q_v = z > -INFINITY ? exp2_near(((double)big_clamp(z) * a.inv_t - L) * kLog2e) : 0.0;
+      if (twice) {
+        for (int j = 0; j < own.n; ++j)
+          if (own.id[j] == own.id[tid] && j != tid) {
+            if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - lp) * kLog2e);
+            if (j < tid) own_at = -1;
+          }
+      }
+      own_grad = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
     }
   }
   __syncthreads();  // the entries' logits are read
@@ -702,7 +720,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
     if (vec < all) write_vector<T, true>(out + vec * N, d.V - vec * N, q[i], a.c, st.n, coef, guard);
   }
   __syncthreads();
-  if (live && tid < own.n && firsts[tid]) store_grad(out + own.id[tid], grads[tid]);
+  if (own_at >= 0) store_grad(out + own_at, own_grad);
 }
 
 int vectors_of(const domino_distill_t& d) { return d.dtype == DOMINO_DTYPE_F32 ? (d.V + 3) / 4 : (d.V + 7) / 8; }

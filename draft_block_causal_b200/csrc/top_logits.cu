@@ -116,6 +116,28 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t o, int warps, int k, Top
 
 __device__ __forceinline__ uint32_t order_bits(uint64_t key) { return (uint32_t)(key >> 32); }
 
+// Cuts the list's n keys to those that reach an order which k of them reach, and returns how many are left.  Every
+// thread looks at the largest of its share of the keys, one in kThreads.
+constexpr int kSlots = kList / kThreads;
+__device__ __forceinline__ int cut_list(TopShared& sh, int n, int k) {
+  uint64_t key[kSlots];
+  uint32_t o = 0;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int at = threadIdx.x + i * kThreads;
+    key[i] = at < n ? sh.list[at] : 0;
+    o = max(o, order_bits(key[i]));
+  }
+  const uint32_t bar = reached_by(o, min(n, kThreads) / 32, k, sh);
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (key[i] != 0 && order_bits(key[i]) >= bar) sh.list[atomicAdd(&sh.count, 1)] = key[i];
+  __syncthreads();
+  return sh.count;
+}
+
 // f(key, rank) for each of the list's n keys below rank k.
 template <typename F>
 __device__ __forceinline__ void rank_list(TopShared& sh, int n, int k, F f) {
@@ -302,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
   if (cluster > 1) {
     const int bits = share_bits(cluster), share = 1 << bits;
     if (held > share) {  // the k largest alone
-      constexpr int kSlots = kList / kThreads;
       uint64_t own[kSlots];
       int place[kSlots];
       int i = 0;
@@ -342,6 +363,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
       if ((i & (share - 1)) < sh.handed[i >> bits] && order_bits(handed[i]) >= bar) sh.list[atomicAdd(&sh.count, 1)] = handed[i];
     __syncthreads();
     held = sh.count;
+    // ranking takes held * held comparisons: many blocks' bars are each far below the row's
+    if (held > a.k + a.k / 2 + 32) held = cut_list(sh, held, a.k);
     if (tid == 0) {
       for (int c = 1; c < cluster; ++c) {
         ref = fmaxf(ref, sh.ref[c][0]);
