@@ -327,7 +327,8 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double m
   const double L = from_top ? kLn2 * (log2(o.all) + (double)t.tn) : l_rest;
   const double lp = a.d.teacher_lse ? my : my + log(t.z);
   const double psum = a.d.teacher_lse ? t.z : 1.0, rho = o.P - psum;
-  const double loss = t.a / o.zn - psum * lp + psum * L + (rho > 0.0 ? rho * (o.outside < 1e-300 ? log(rho) - l_rest + L : log(rho / o.outside)) : 0.0);
+  const double of_rho = o.outside < 1e-300 ? log(rho) - l_rest + L : log(rho / o.outside);
+  const double loss = t.a / o.zn - psum * lp + psum * L + (rho > 0.0 ? rho * of_rho : 0.0);
   a.loss[r] = (float)(o.scale / a.inv_t * loss);
   if (a.stats) {
     Stats st;
@@ -387,8 +388,8 @@ __device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const 
   cluster_store(at + 40, __float_as_int(t.tn));
 }
 
-// Marks: a word for each thread and tile, with a byte for each of its kVecs vectors there and a bit for each column of
-// an entry.  One warp clears those of `vecs` vectors and sets its block's entries'.
+// Marks: a word for each thread and tile, with a byte for each of its kVecs vectors there and a bit for each column
+// of an entry.  One warp clears those of `vecs` vectors and sets its block's entries'.
 constexpr int kThreads = 256;
 constexpr int kPerSm = 4;         // blocks an SM
 constexpr int kData = kThreads - 32;
@@ -425,7 +426,8 @@ __device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
       const float2 x = fma2(make_float2(z[e], z[e + 1]), c2, n2);
-      const float2 t = CHECK ? make_float2(fmaxf(ex2(x.x), 0.f), fmaxf(ex2(x.y), 0.f)) : make_float2(ex2(x.x), ex2(x.y));
+      const float2 t = CHECK ? make_float2(fmaxf(ex2(x.x), 0.f), fmaxf(ex2(x.y), 0.f))
+                             : make_float2(ex2(x.x), ex2(x.y));
       const float2 y = mul2(t, k2);
       z[e] = y.x;
       z[e + 1] = y.y;
@@ -453,20 +455,19 @@ __device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q
 }
 
 // Named barriers of a block, for warps that go different ways (0 is __syncthreads): `n` threads arrive or wait.
-template <int ID> __device__ __forceinline__ void bar_arrive(int n) { asm volatile("bar.arrive %0, %1;" ::"n"(ID), "r"(n) : "memory"); }
-template <int ID> __device__ __forceinline__ void bar_wait(int n) { asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(n) : "memory"); }
+template <int ID>
+__device__ __forceinline__ void bar_arrive(int n) {
+  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "r"(n) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void bar_wait(int n) {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(n) : "memory");
+}
 
-// Loss, and gradient (G not void), of one row a cluster.  Data warps stream the slice, the next tile's loads in
-// flight while one is worked on; one warp has the entries and the exchange.
-//
-// Bound by memory: V values read once from DRAM and V written.  The second read hits L2 as long as the rows in work
-// take less than about half of it, which the launch sees to with the cluster's size.  (Holding a row in
-// registers or shared memory between the two took longer: 231 us and 346 us where this takes NNN, 1024 rows of
-// 151936 bf16.)
 // A thread's own vectors of a slice, tile after tile.  Ahead in registers, one tile; or, for the gradient, by
 // asynchronous copies into its own places of shared memory, kStages - 1 tiles: no barrier is needed for either.
-// (Loss and gradient of 1024 rows of 151936 bf16: 136 us by registers, 127 by copies; the loss alone of 512 rows
-// fp32, whose larger slices' marks want the shared memory: 48 and 57.)
+// (Loss and gradient of 1024 rows of 151936 bf16: 136 us by registers, 127 by copies, 2 or 4 stages 130 and 147; the
+// loss alone of 512 rows fp32, whose larger slices' marks want the shared memory: 48 by registers and 57.)
 constexpr int kStages = 3;
 constexpr int kRing = kStages * kTile * 16;
 
@@ -529,6 +530,15 @@ struct Copies {
   }
 };
 
+// Loss, and gradient (G not void), of one row a cluster.  Data warps stream the slice, the next tiles on the way while
+// one is worked on; one warp has the entries and the exchange.
+//
+// Bound by memory, then by the exponentials: V values are read once from DRAM and V written; one exponential for the
+// sum and one for the gradient (16 a clock and SM) take two thirds of the memory's time for bf16 in and out, half of
+// it for fp32.  The second read hits L2 while the rows in work take at most 48 MB, which the launch sees to with the
+// cluster's size: 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live rows have.  Measured
+// there: 123 us (584 MB, 4.8 TB/s); holding a row in registers or in shared memory between its sum and its gradient
+// took 231 and 346 us, for the work they leave to few threads.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   constexpr int N = Vec<T>::N;
@@ -656,8 +666,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   }
 }
 
-// The gradient from a row's stats, a chunk of kGradVecs vectors a thread by each block.  The logits may be
-// overwritten: a chunk's entries read theirs first.
+// The gradient from a row's stats, a chunk of kGradVecs vectors a thread by each block, all loaded at once; the chunk's
+// entries are found by one warp and taken by as many threads meanwhile.  The logits may be overwritten: the entries
+// read theirs first.  Bound by memory: forward and backward of 360 rows of 50001 bf16 take 30 us of GPU time together
+// for 104 MB, of which the two kernels' starts and the entries' chains of loads are a third.
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 8;
 

@@ -7,11 +7,16 @@
 // threads' maxima reach has k values at or above it, and not many more than k, as a thread's second largest is
 // rarely among them.  It is raised after 1, 3, 9, 27, ... tiles only, so that between them no thread waits for
 // another; each such stretch notes about 2k vectors.  A value in a later tile, whose column is higher, has to
-// exceed the bar.  At the end the noted vectors are read again, by all threads alike, and their values that reach
-// the last bar become the list of candidates: taking them as they are met cost three times the instructions,
-// since they come one lane at a time.  Should there be more than the notes or the list hold (ascending rows, many
-// equal values), the exact k are selected digit by digit from the slice.  The lists go to block 0, with the sums,
-// through distributed shared memory; block 0 cuts them by the highest bar and ranks what is left.
+// exceed the bar.  At the end the noted vectors whose maximum reaches the last bar are read again, by all threads
+// alike, and their values that reach it become the list of candidates: taking them as they are met cost three
+// times the instructions, since they come one lane at a time.  Should there be more than the notes or the list
+// hold (ascending rows, many equal values), the exact k are selected digit by digit from the slice.  The lists go
+// to block 0, with the sums, through distributed shared memory; block 0 cuts them and ranks what is left.
+//
+// Bound by memory: 512 rows of 151936 fp32 take 51 us for k = 8 (6.1 TB/s, 93% of the measured copy rate) and 58 us
+// for k = 64, whose notes and ranking come after all blocks' reads; bf16 rows by the exponentials as well, one a
+// value at 16 a clock and SM (1024 rows of 151936: 62 us, 5.0 TB/s).  One row of 151936 fp32 over 16 blocks: 9 us,
+// all latency.
 #include "cluster.cuh"
 #include "launch.cuh"
 #include "vocab_rows.cuh"
@@ -37,7 +42,7 @@ __host__ __device__ constexpr int share_bits(int cluster) { return cluster > 8 ?
 struct TopShared {
   alignas(16) uint64_t list[kList + 1];
   union {
-    uint32_t notes[kNotes];
+    uint2 notes[kNotes];        // a vector, and the order of its maximum
     uint32_t digits[kDigits];
   };
   double sum[kMaxCluster];     // block 0: every block's sum ...
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
         for (int i = 0; i < kVecs; ++i)
           if (vm[i] >= floor) {
             const int to = atomicAdd(&sh.noted, 1);
-            if (to < kNotes) sh.notes[to] = t0 + i * kThreads + tid;
+            if (to < kNotes) sh.notes[to] = make_uint2(t0 + i * kThreads + tid, order_of(vm[i]));
           }
       }
     }
@@ -301,7 +306,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
   bool exact = held > kNotes;
   if (!exact) {
     for (int i = tid; i < held; i += kThreads) {
-      const int vec = sh.notes[i];
+      const uint2 note = sh.notes[i];
+      if (note.y < bar) continue;
+      const int vec = (int)note.x;
       float z[N];
       widen(__ldcg(reinterpret_cast<const uint4*>(row) + vec), z);
 #pragma unroll
@@ -402,8 +409,11 @@ cudaError_t launch_top_rows(const TopRows& a, cudaStream_t st) {
   while (cluster < kMaxCluster && 2 * cluster * (int64_t)a.rows <= 4 * 148 && vecs / (2 * cluster) >= 2 * kThreads) cluster *= 2;
   const dim3 grid((unsigned)a.rows * (unsigned)cluster);
   const size_t smem = cluster > 1 ? ((size_t)cluster << share_bits(cluster)) * sizeof(uint64_t) : 0;
-  return note_launch(f ? launch_cluster(k_top_rows<float>, cluster, grid, dim3(kThreads), smem, st, a, cluster)
-                       : launch_cluster(k_top_rows<bf16>, cluster, grid, dim3(kThreads), smem, st, a, cluster));
+  auto kern = f ? k_top_rows<float> : k_top_rows<bf16>;
+  // with the static part more than a block has by default; the same for all calls, of several host threads too
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kList * sizeof(uint64_t));
+  if (e != cudaSuccess) return e;
+  return note_launch(launch_cluster(kern, cluster, grid, dim3(kThreads), smem, st, a, cluster));
 }
 
 }  // namespace domino

@@ -173,26 +173,6 @@ __device__ __forceinline__ uint64_t select_key(uint32_t order, int v) {
   return order ? (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(v)) : 0ull;
 }
 
-// Block sums and maxima in a fixed order; red has one slot per warp, all threads get the result.
-template <typename F, typename Op>
-__device__ __forceinline__ F block_reduce(F v, F* red, Op op) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  F r = red[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) r = op(r, red[w]);
-  return r;
-}
-struct MaxOp {
-  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
-  __device__ double operator()(double a, double b) const { return fmax(a, b); }
-};
-struct AddOp {
-  template <typename F> __device__ F operator()(F a, F b) const { return a + b; }
-};
-
 // log of sum * 2^n (natural), with the correction for c's rounding; m: the row's maximum.
 constexpr double kLn2 = 0.693147180559945309417232;
 constexpr double kLog2e = 1.44269504088896340735992;
