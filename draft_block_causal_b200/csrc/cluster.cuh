@@ -16,8 +16,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // Every thread of every block of the cluster calls both; stores before the arrival, into other blocks'
 // shared memory too, are visible after the wait.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Address of `p`, a shared-memory variable of this kernel, in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {

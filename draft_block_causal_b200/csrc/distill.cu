@@ -417,7 +417,8 @@ __device__ __forceinline__ void store_grad(bf16* p, float x) { *p = __float2bflo
 // Writes one vector's gradient, coef * 2^(c z - n), the first `columns` of it.  CHECK: its values may be NaN without
 // guard saying so.
 template <typename T, bool CHECK = false, typename G>
-__device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q, float c, float n, float coef, bool guard) {
+__device__ __forceinline__ void write_vector(G* out, int columns, const uint4& q, float c, float n, float coef,
+                                             bool guard) {
   constexpr int N = Vec<T>::N;
   float z[N];
   widen(q, z);
@@ -747,7 +748,8 @@ cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
   // that few rows use every SM; and to keep the rows in work in about 48 MB of L2
   while (cluster < kMaxCluster &&
          (vecs > cluster * kSlice || (2 * cluster * (int64_t)a.d.rows <= blocks && vecs / (2 * cluster) >= 2 * kData) ||
-          (a.grad && std::min<int64_t>(a.d.rows, blocks / cluster) * vecs * 16 > (48 << 20) && vecs / (2 * cluster) >= 2 * kData)))
+          (a.grad && std::min<int64_t>(a.d.rows, blocks / cluster) * vecs * 16 > (48 << 20) &&
+           vecs / (2 * cluster) >= 2 * kData)))
     cluster *= 2;
   a.cluster = cluster;
   const int smem = (a.grad ? kRing : 0) + ((vecs + cluster - 1) / cluster + kTile - 1) / kTile * kTile;
@@ -775,7 +777,8 @@ int check_distill(const domino_distill_t* d) {
   if (!d || !rows_ok(d->rows, d->V, d->ld, d->dtype, d->logits)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (d->K < 1 || d->K > DOMINO_MAX_TOP || !temperature_ok(d->temperature)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (!d->top_ids || !d->top_logits) return DOMINO_ERR_INVALID_ARGUMENT;
-  for (const void* q : {(const void*)d->top_ids, (const void*)d->top_logits, (const void*)d->teacher_lse, (const void*)d->row_weights})
+  for (const void* q : {(const void*)d->top_ids, (const void*)d->top_logits, (const void*)d->teacher_lse,
+                        (const void*)d->row_weights})
     if (!aligned4(q)) return DOMINO_ERR_INVALID_ARGUMENT;
   if (d->rows > DOMINO_MAX_ROWS) return DOMINO_ERR_UNSUPPORTED;
   return DOMINO_OK;
@@ -783,16 +786,18 @@ int check_distill(const domino_distill_t* d) {
 
 // The checks of a call's outputs: alignment, and that no two of them, nor one and an input, share memory -- but
 // for a gradient in the place of the logits.  grad_loss: another input, or null.
-int check_outputs(const domino_distill_t& d, const float* loss, const float* stats, bool stats_out, const float* grad_loss,
-                  const void* grad, int64_t grad_ld, int grad_dtype) {
-  if (!aligned4(loss) || !aligned4(grad_loss) || (reinterpret_cast<uintptr_t>(stats) & 15u)) return DOMINO_ERR_INVALID_ARGUMENT;
+int check_outputs(const domino_distill_t& d, const float* loss, const float* stats, bool stats_out,
+                  const float* grad_loss, const void* grad, int64_t grad_ld, int grad_dtype) {
+  if (!aligned4(loss) || !aligned4(grad_loss) || (reinterpret_cast<uintptr_t>(stats) & 15u))
+    return DOMINO_ERR_INVALID_ARGUMENT;
   if (grad && !rows_ok(d.rows, d.V, grad_ld, grad_dtype, grad)) return DOMINO_ERR_INVALID_ARGUMENT;
   const size_t rows = (size_t)d.rows, e = rows * d.K * 4, in_bytes = rows_span(d.rows, d.V, d.ld, d.dtype);
   const size_t grad_bytes = grad ? rows_span(d.rows, d.V, grad_ld, grad_dtype) : 0;
   const bool in_place = grad == d.logits && grad_ld == d.ld && grad_dtype == d.dtype;
   const Range ids{d.top_ids, e}, tops{d.top_logits, e}, lse{d.teacher_lse, rows * 4}, w{d.row_weights, rows * 4},
       given{stats_out ? nullptr : stats, rows * 32}, up{grad_loss, rows * 4};
-  if (!disjoint({{loss, rows * 4}, {stats_out ? stats : nullptr, rows * 32}, {grad, grad_bytes}}, {ids, tops, lse, w, given, up}) ||
+  if (!disjoint({{loss, rows * 4}, {stats_out ? stats : nullptr, rows * 32}, {grad, grad_bytes}},
+                {ids, tops, lse, w, given, up}) ||
       !disjoint({{loss, rows * 4}, {stats_out ? stats : nullptr, rows * 32}, {in_place ? nullptr : grad, grad_bytes}},
                 {{d.logits, in_bytes}}))
     return DOMINO_ERR_INVALID_ARGUMENT;

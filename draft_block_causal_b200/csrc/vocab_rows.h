@@ -1,4 +1,4 @@
-// vocab_rows.h -- host-side checks and the row scan shared by the operators on rows of logits.
+// vocab_rows.h -- host-side checks and the row scan's launch shared by the operators on rows of logits.
 #pragma once
 
 #include "internal.h"

@@ -138,7 +138,7 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
         L.domino_accept_sample.restype = ctypes.c_int
         L.domino_top_logits.argtypes = [i32, i32, ctypes.c_int64, i32, vp, i32, ctypes.c_float, vp, vp, vp, vp]
         L.domino_top_logits.restype = ctypes.c_int
-        L.domino_beam_workspace_bytes.argtypes = [i32, i32, i32]
+        L.domino_beam_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         L.domino_beam_workspace_bytes.restype = sz
         L.domino_beam_select.argtypes = [ctypes.POINTER(BeamArgs), vp, sz, vp]
         L.domino_beam_select.restype = ctypes.c_int
@@ -621,8 +621,8 @@ def _logit_rows(t, name: str):
     if ld is None:  # a single row
         ld = padded
     if (strides[-1] != 1 and V > 1) or ld < V or ld % 8:
-        raise ValueError(f"the rows of {name} must be contiguous and a multiple of 8 values apart (stride {ld}, V {V}): "
-                         f"pad the vocabulary's storage")
+        raise ValueError(f"the rows of {name} must be contiguous and a multiple of 8 values apart (stride {ld}, "
+                         f"V {V}): pad the vocabulary's storage")
     if padded != V:
         rows = t.numel() // V
         if (t.storage_offset() + (rows - 1) * ld + padded) * t.element_size() > t.untyped_storage().nbytes():
@@ -690,8 +690,9 @@ def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_ou
     return values_out, ids_out, lse_out
 
 
-def beam_workspace_bytes(B: int, W_in: int, W_out: int) -> int:
-    return int(lib().domino_beam_workspace_bytes(int(B), int(W_in), int(W_out)))
+def beam_workspace_bytes(B: int, W_in: int, W_out: int, V: int, dtype=torch.float32) -> int:
+    """Bytes of workspace that beam_select takes for logits [B, W_in, V] of ``dtype``: 0 for small calls."""
+    return int(lib().domino_beam_workspace_bytes(int(B), int(W_in), int(W_out), int(V), _DTYPE_CODE[dtype]))
 
 
 class BeamStep(NamedTuple):
@@ -754,17 +755,18 @@ def beam_select(logits, scores, beams: int, states=None, history=None, pos: int 
                 _expect(t, f"out.{name}", dims, dt, dev)
         if out.finished is not None:
             _expect(out.finished, "out.finished", (B, n), torch.uint8, dev)
+    nbytes = 0
     if workspace is None:
-        nbytes = beam_workspace_bytes(B, W, n)
-        if nbytes == 0:
-            raise DominoError(ERR_UNSUPPORTED, "domino_beam_workspace_bytes")
-        workspace = _new(scores, (nbytes,), torch.uint8, stream)
+        nbytes = lib().domino_beam_workspace_bytes(B, W, n, V, code)
+        if nbytes:
+            workspace = _new(scores, (nbytes,), torch.uint8, stream)
     else:
         _expect_workspace(workspace, dev)
+        nbytes = workspace.numel()
     a = BeamArgs(B, W, n, V, ld, code, int(eos), Hs, hist_len, int(pos), logits.data_ptr(), scores.data_ptr(),
                  _data(finished), _data(states), _data(history), out.scores.data_ptr(), out.parents.data_ptr(),
                  out.tokens.data_ptr(), _data(out.finished), _data(out.states), _data(out.history))
-    rc = _launch(dev, lib().domino_beam_select, ctypes.byref(a), workspace.data_ptr(), workspace.numel(), sp)
+    rc = _launch(dev, lib().domino_beam_select, ctypes.byref(a), _data(workspace), nbytes, sp)
     _check(rc, "domino_beam_select")
     return out
 

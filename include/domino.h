@@ -248,8 +248,9 @@ DOMINO_API int domino_accept_sample(int32_t B, int32_t L, int32_t V, const int32
  *
  * They read logits as `rows` rows of V values, fp32 or bf16 (`dtype`), `ld` values apart: V may be
  * any number from 1 to DOMINO_MAX_V and need not be a multiple of 8, but ld must be (ld >= V), the
- * base must be 16-byte aligned (the other arrays to their elements), and V rounded up to a multiple of 8 values must be readable in every
- * row (what lies there is ignored, and never written).  rows <= DOMINO_MAX_ROWS.
+ * base must be 16-byte aligned (the other arrays to their elements), and V rounded up to a multiple
+ * of 8 values must be readable in every row (what lies there is ignored, and never written).
+ * rows <= DOMINO_MAX_ROWS.
  *
  * A logit of -infinity is a barred token: it has no mass and is never selected.  NaN counts as
  * -infinity.  In sums and scores a magnitude above 1e6 (+infinity, the type's lowest value) counts as
@@ -290,7 +291,8 @@ DOMINO_API int domino_top_logits(int32_t rows, int32_t V, int64_t ld, int32_t dt
  *   -infinity, parent 0, token 0, finished 0.
  * No output may overlap an input or another (DOMINO_ERR_INVALID_ARGUMENT).  1 <= W_in, W_out <=
  * DOMINO_MAX_BEAMS; Hs and hist_len up to 2^20 (else DOMINO_ERR_UNSUPPORTED).
- * Needs domino_beam_workspace_bytes(B, W_in, W_out) bytes of workspace (256-byte aligned). */
+ * Needs domino_beam_workspace_bytes bytes of workspace (256-byte aligned); 0: none (and 0 for invalid
+ * sizes). */
 typedef struct {
   int32_t B, W_in, W_out, V;
   int64_t ld;
@@ -307,7 +309,7 @@ typedef struct {
   int32_t* history_out;
 } domino_beam_t;
 
-DOMINO_API size_t domino_beam_workspace_bytes(int32_t B, int32_t W_in, int32_t W_out);
+DOMINO_API size_t domino_beam_workspace_bytes(int32_t B, int32_t W_in, int32_t W_out, int32_t V, int32_t dtype);
 DOMINO_API int domino_beam_select(const domino_beam_t* beam, void* workspace, size_t workspace_bytes,
                                   domino_stream_t stream);
 

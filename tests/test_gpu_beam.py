@@ -16,7 +16,7 @@ def check(logits, scores, n, **kw):
     B, W, V = logits.shape
     got = domino.beam_select(logits, scores, n, **kw)
     torch.cuda.synchronize()
-    host = {k: (v.cpu().numpy() if isinstance(v, torch.Tensor) else v) for k, v in kw.items()}
+    host = {k: (v.cpu().numpy() if isinstance(v, torch.Tensor) else v) for k, v in kw.items() if k != "workspace"}
     want = R.beam(logits.double().cpu().numpy(), scores.double().cpu().numpy(), n, **host)
     np.testing.assert_array_equal(got.parents.cpu().numpy(), want["parents"])
     np.testing.assert_array_equal(got.tokens.cpu().numpy(), want["tokens"])
@@ -43,7 +43,10 @@ def inputs(B, W, V, dtype, Hs=24, hist=9, seed=0):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("B,W,n,V", [(1, 1, 1, 1), (1, 1, 8, 5), (2, 3, 32, 4), (1, 4, 4, 151936), (5, 7, 3, 20011),
-                                     (40, 1, 8, 5000), (3, 32, 32, 3000), (64, 8, 8, 2500), (2, 32, 1, 1003)])
+                                     (40, 1, 8, 5000), (3, 32, 32, 3000), (64, 8, 8, 2500), (2, 32, 1, 1003),
+                                      (2, 17, 9, 30001), (1, 16, 32, 9000), (3, 3, 5, 70000), (1, 5, 2, 40000),
+                                      (300, 2, 4, 1500), (1, 1, 32, 151936), (32, 8, 8, 40000), (4, 32, 32, 70000),
+                                      (70, 1, 9, 151936)])
 def test_random_beams(B, W, n, V, dtype):
     z, sc, st, hi = inputs(B, W, V, dtype)
     check(z, sc, n, states=st, history=hi, pos=4)
@@ -59,8 +62,11 @@ def test_state_and_history_sizes(Hs, hist, pos):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-def test_finished_and_dead_beams(dtype):
-    B, W, V, eos = 6, 5, 1203, 1202
+@pytest.mark.parametrize("B,V", [(6, 1203), (90, 40003)], ids=["one-kernel", "two-kernels"])
+def test_finished_and_dead_beams(B, V, dtype):
+    W, eos = 5, V - 1
+    code = {"fp32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    assert (domino.beam_workspace_bytes(B, W, 6, V, code) > 0) == (B == 90)
     z, sc, st, hi = inputs(B, W, V, dtype)
     sc[0, :] = -np.inf                   # a dead group
     sc[1, 1:] = -np.inf                  # one beam alive
@@ -78,17 +84,19 @@ def test_finished_and_dead_beams(dtype):
     check(z, sc, 6, states=st, history=hi, pos=8, eos=eos)
 
 
-def test_equal_scores_go_to_the_lower_beam_and_token():
-    z = torch.zeros(2, 4, 64, device="cuda")
-    z[1] = 1.0 + torch.arange(64, device="cuda") % 2
-    sc = torch.full((2, 4), -1.5, device="cuda")
+@pytest.mark.parametrize("B,V", [(2, 64), (400, 8192)], ids=["one-kernel", "two-kernels"])
+def test_equal_scores_go_to_the_lower_beam_and_token(B, V):
+    z = torch.zeros(B, 4, V, device="cuda")
+    z[1] = 1.0 + torch.arange(V, device="cuda") % 2
+    sc = torch.full((B, 4), -1.5, device="cuda")
     got = check(z, sc, 10)
     assert got.parents[0].tolist() == [0] * 10 and got.tokens[0].tolist() == list(range(10))
     assert got.tokens[1].tolist() == list(range(1, 21, 2))
 
 
-def test_barred_and_extreme_logits():
-    B, W, V = 2, 3, 900
+@pytest.mark.parametrize("B,V", [(2, 900), (2, 70000), (60, 50000)], ids=["one-kernel", "parts", "two-kernels"])
+def test_barred_and_extreme_logits(B, V):
+    W = 3
     z, sc, st, hi = inputs(B, W, V, "fp32")
     z[0, 0, 5:] = float("-inf")
     z[0, 1, :] = torch.finfo(torch.float32).min
@@ -102,19 +110,24 @@ def test_given_outputs_workspace_and_strides():
     z, sc, st, hi = inputs(4, 3, 2000, "bf16")
     want = domino.beam_select(z, sc, 5, states=st, history=hi, pos=1)
     out = domino.BeamStep(*(None if t is None else torch.zeros_like(t) for t in want))
-    ws = domino.alloc_workspace(domino.beam_workspace_bytes(4, 3, 5))
-    ws.fill_(255)
-    got = domino.beam_select(z, sc, 5, states=st, history=hi, pos=1, out=out, workspace=ws)
+    assert domino.beam_workspace_bytes(4, 3, 5, 2000, torch.bfloat16) == 0
+    got = domino.beam_select(z, sc, 5, states=st, history=hi, pos=1, out=out)
     torch.cuda.synchronize()
     assert got is out
     for a, b in zip(got, want):
         assert (a is None and b is None) or torch.equal(a, b)
+    z, sc, st, hi = inputs(20, 4, 151936, "fp32")  # in two kernels
+    ws = domino.alloc_workspace(domino.beam_workspace_bytes(20, 4, 5, 151936))
+    assert ws.numel() > 0
+    ws.fill_(255)
+    check(z, sc, 5, states=st, history=hi, pos=1, workspace=ws)
+    sc, st, hi = (t[:4, :3].contiguous() for t in (sc, st, hi))
     wide = torch.randn(4, 3, 4096, device="cuda")
     check(wide[..., 24:2023], sc, 5, states=st)
     check(torch.randn(4, 6, 1000, device="cuda")[:, :1], sc[:, :1].contiguous(), 5)
 
 
-def test_on_another_stream_and_in_two_graphs_with_their_own_workspaces():
+def test_on_another_stream_and_in_two_graphs():
     z, sc, st, hi = inputs(8, 4, 6000, "fp32")
     want = domino.beam_select(z, sc, 4, states=st, history=hi, pos=3)
     torch.cuda.synchronize()

@@ -1,5 +1,5 @@
-"""The operators on rows of logits as they are used together with the head: a distillation step from a target's logits to
-the gradient of the base logits, and beam drafting of a block through teacher-forced steps, against the fp64 oracle.
+"""The operators on rows of logits as they are used together with the head: a distillation step from a target's logits
+to the gradient of the base logits, and beam drafting of a block through teacher-forced steps, against the fp64 oracle.
 
 The head's logits are within 1e-2 + 1e-2 |z| of the oracle's (gpu_common).  A difference of e in every logit moves a
 log-probability by at most 2e and a probability by the factor exp(2e)."""

@@ -30,8 +30,8 @@ def top(L, **kw):
                                  dict(ld=1001), dict(ld=992), dict(dtype=2), dict(dtype=-1), dict(logits=None),
                                  dict(logits=P + 8), dict(k=0), dict(k=129), dict(T=0.0), dict(T=-1.0), dict(T=1e-4),
                                  dict(T=1025.0), dict(T=float("nan")), dict(T=float("inf")), dict(values=None),
-                                 dict(ids=None), dict(values=P + 4 * 3999), dict(ids=P), dict(lse=P + 4), dict(values=P + STEP + 2),
-                                 dict(ids=P + 2 * STEP + 1), dict(lse=P + 3 * STEP + 3), dict(lse=P + STEP + 16),
+                                 dict(ids=None), dict(values=P + 4 * 3999), dict(ids=P), dict(lse=P + 4),
+                                 dict(values=P + STEP + 2), dict(ids=P + 2 * STEP + 1), dict(lse=P + 3 * STEP + 3), dict(lse=P + STEP + 16),
                                  dict(ids=P + STEP + 4)])
 def test_top_logits_refusals(L, bad):
     assert top(L, **bad) == domino.ERR_INVALID_ARGUMENT
@@ -60,20 +60,27 @@ def beam(L, ws=P + 20 * STEP, ws_bytes=1 << 40, **kw):
                                  dict(Hs=62), dict(Hs=0), dict(states=P + 2 * STEP + 4), dict(hist_len=0), dict(pos=-1),
                                  dict(pos=16), dict(states_out=P + 2 * STEP), dict(history_out=P + 3 * STEP + 64),
                                  dict(scores_out=P + STEP), dict(tokens_out=P + 3 * STEP),
-                                 dict(parents_out=P + 20 * STEP), dict(scores=P + STEP + 2),
+                                 dict(scores=P + STEP + 2),
                                  dict(tokens_out=P + 6 * STEP + 1), dict(history=P + 3 * STEP + 2),
                                  dict(tokens_out=P + 5 * STEP), dict(scores_out=P + 7 * STEP + 4)])
 def test_beam_select_refusals(L, bad):
     assert beam(L, **bad) == domino.ERR_INVALID_ARGUMENT
 
 
-def test_beam_select_workspace_and_limits(L):
-    n = L.domino_beam_workspace_bytes(2, 3, 4)
+def test_beam_select_limits(L):
+    assert L.domino_beam_select(None, None, 0, None) == domino.ERR_INVALID_ARGUMENT
+    assert L.domino_beam_workspace_bytes(2, 3, 4, 1000, 1) == 0  # small: none is needed
+    n = L.domino_beam_workspace_bytes(200, 3, 4, 100000, 0)
     assert n > 0 and n % 256 == 0
-    for w, b in ((None, n), (P + 20 * STEP + 16, n), (P + 20 * STEP, n - 1)):
-        assert beam(L, ws=w, ws_bytes=b) == domino.ERR_WORKSPACE
-    assert L.domino_beam_select(None, P, n, None) == domino.ERR_INVALID_ARGUMENT
-    for bad in ((0, 3, 4), (2, 0, 4), (2, 3, 33), (1 << 22, 3, 4)):
+    big = dict(B=200, V=100000, ld=100000, dtype=0, states=None, states_out=None, history=None, history_out=None,
+               scores=P + 21 * STEP)
+    far = {k: P + i * 1000 * STEP for i, k in enumerate(("scores", "scores_out", "parents_out", "tokens_out"), 1)}
+    big.update(far)
+    for w, b in ((None, n), (P + 9000 * STEP + 16, n), (P + 9000 * STEP, n - 1)):
+        assert beam(L, ws=w, ws_bytes=b, **big) == domino.ERR_WORKSPACE
+    assert beam(L, ws=far["tokens_out"], ws_bytes=n, **big) == domino.ERR_INVALID_ARGUMENT
+    for bad in ((0, 3, 4, 100000, 0), (2, 0, 4, 100000, 0), (2, 3, 33, 100000, 0), (1 << 22, 3, 4, 100000, 0),
+                (200, 3, 4, 0, 0)):
         assert L.domino_beam_workspace_bytes(*bad) == 0
     assert beam(L, Hs=(1 << 20) + 4) == domino.ERR_UNSUPPORTED
     assert beam(L, hist_len=(1 << 20) + 1) == domino.ERR_UNSUPPORTED
@@ -104,7 +111,8 @@ BOTH = [dict(rows=0), dict(V=0), dict(ld=1004), dict(ld=992), dict(dtype=5), dic
 
 
 @pytest.mark.parametrize("bad", BOTH + [dict(loss=None), dict(loss=P), dict(stats=P),
-                                        dict(stats=P + 5 * STEP), dict(grad=P + 5 * STEP), dict(loss=P + STEP), dict(loss=P + 5 * STEP + 2)])
+                                        dict(stats=P + 5 * STEP), dict(grad=P + 5 * STEP), dict(loss=P + STEP),
+                                        dict(loss=P + 5 * STEP + 2)])
 def test_distill_refusals(L, bad):
     assert distill(L, **bad) == domino.ERR_INVALID_ARGUMENT
 
