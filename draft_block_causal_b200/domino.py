@@ -691,7 +691,10 @@ def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_ou
 
 
 def beam_workspace_bytes(B: int, W_in: int, W_out: int, V: int, dtype=torch.float32) -> int:
-    """Bytes of workspace that beam_select takes for logits [B, W_in, V] of ``dtype``: 0 for small calls."""
+    """Bytes of workspace that beam_select takes for logits [B, W_in, V] of ``dtype``: 0 for small calls (and for
+    sizes that it does not take)."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype is {dtype}, expected torch.float32 or torch.bfloat16")
     return int(lib().domino_beam_workspace_bytes(int(B), int(W_in), int(W_out), int(V), _DTYPE_CODE[dtype]))
 
 
@@ -887,7 +890,9 @@ class _DistillLoss(torch.autograd.Function):
 def distill_loss(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 1.0, row_weights=None,
                  status=None):
     """``distill``'s loss as a differentiable function of ``logits``, on the current stream: [...] fp32, one per row.
-    The teacher's tensors and the row weights are constants: one that requires a gradient is refused."""
+    The teacher's tensors and the row weights are constants: one that requires a gradient is refused.  To capture a
+    step with its backward pass into a CUDA graph, run it once on the capturing stream first and drop what earlier
+    steps of the same leaves have returned: their nodes belong to another stream."""
     for name, t in (("top_logits", top_logits), ("teacher_lse", teacher_lse), ("row_weights", row_weights)):
         if isinstance(t, torch.Tensor) and t.requires_grad:
             raise ValueError(f"{name} requires a gradient, which distill_loss does not give")

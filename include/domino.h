@@ -291,8 +291,8 @@ DOMINO_API int domino_top_logits(int32_t rows, int32_t V, int64_t ld, int32_t dt
  *   -infinity, parent 0, token 0, finished 0.
  * No output may overlap an input or another (DOMINO_ERR_INVALID_ARGUMENT).  1 <= W_in, W_out <=
  * DOMINO_MAX_BEAMS; Hs and hist_len up to 2^20 (else DOMINO_ERR_UNSUPPORTED).
- * Needs domino_beam_workspace_bytes bytes of workspace (256-byte aligned); 0: none (and 0 for invalid
- * sizes). */
+ * Needs domino_beam_workspace_bytes bytes of workspace (256-byte aligned), of its own while another call
+ * is in flight; 0: none (and 0 for invalid sizes). */
 typedef struct {
   int32_t B, W_in, W_out, V;
   int64_t ld;

@@ -127,8 +127,10 @@ def test_given_outputs_workspace_and_strides():
     check(torch.randn(4, 6, 1000, device="cuda")[:, :1], sc[:, :1].contiguous(), 5)
 
 
-def test_on_another_stream_and_in_two_graphs():
-    z, sc, st, hi = inputs(8, 4, 6000, "fp32")
+@pytest.mark.parametrize("B,V", [(8, 6000), (40, 70000)], ids=["one-kernel", "two-kernels"])
+def test_on_another_stream_and_in_two_graphs(B, V):
+    z, sc, st, hi = inputs(B, 4, V, "fp32")
+    assert (domino.beam_workspace_bytes(B, 4, 4, V) > 0) == (B == 40)
     want = domino.beam_select(z, sc, 4, states=st, history=hi, pos=3)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()

@@ -71,7 +71,9 @@ def test_beam_select_limits(L):
     assert L.domino_beam_select(None, None, 0, None) == domino.ERR_INVALID_ARGUMENT
     assert L.domino_beam_workspace_bytes(2, 3, 4, 1000, 1) == 0  # small: none is needed
     n = L.domino_beam_workspace_bytes(200, 3, 4, 100000, 0)
-    assert n > 0 and n % 256 == 0
+    assert n > 0 and n % 256 == 0 and domino.beam_workspace_bytes(200, 3, 4, 100000) == n
+    with pytest.raises(ValueError, match="dtype"):
+        domino.beam_workspace_bytes(200, 3, 4, 100000, torch.float16)
     big = dict(B=200, V=100000, ld=100000, dtype=0, states=None, states_out=None, history=None, history_out=None,
                scores=P + 21 * STEP)
     far = {k: P + i * 1000 * STEP for i, k in enumerate(("scores", "scores_out", "parents_out", "tokens_out"), 1)}
