@@ -84,25 +84,33 @@ struct OwnSums {
   double ts, z, a;   // as in Record
 };
 
-// One warp: a row's entries, one k = 32 i + lane after the other, for the block with columns [v0, v1).  Ends with the
-// warp's barrier.
-__device__ __forceinline__ void find_own(const DistillArgs& a, int r, int v0, int v1, Own& own, bool report) {
-  const domino_distill_t& d = a.d;
-  const int lane = threadIdx.x & 31;
+// A row's entries, k = 32 i + lane, as one warp reads them.
+struct Teacher {
   int32_t id[kEach];
-  float t[kEach], most = -INFINITY;
-  const float lse = d.teacher_lse ? d.teacher_lse[r] : 0.f;
+  float t[kEach], lse;
+};
+__device__ __forceinline__ void read_teacher(const domino_distill_t& d, int r, Teacher& in) {
+  in.lse = d.teacher_lse ? d.teacher_lse[r] : 0.f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    if (32 * i >= d.K) break;
-    const int k = 32 * i + lane;
-    id[i] = -1;
-    t[i] = -INFINITY;
+    const int k = 32 * i + (threadIdx.x & 31);
+    in.id[i] = -1;
+    in.t[i] = -INFINITY;
     if (k < d.K) {
-      id[i] = __ldg(d.top_ids + (size_t)r * d.K + k);
-      t[i] = __ldg(d.top_logits + (size_t)r * d.K + k);
+      in.id[i] = __ldg(d.top_ids + (size_t)r * d.K + k);
+      in.t[i] = __ldg(d.top_logits + (size_t)r * d.K + k);
     }
   }
+}
+
+// One warp: those for the block with columns [v0, v1).  Ends with the warp's barrier.
+__device__ __forceinline__ void find_own(const DistillArgs& a, Teacher& in, int v0, int v1, Own& own, bool report) {
+  const domino_distill_t& d = a.d;
+  const int lane = threadIdx.x & 31;
+  int32_t(&id)[kEach] = in.id;
+  const float(&t)[kEach] = in.t;
+  const float lse = in.lse;
+  float most = -INFINITY;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -256,7 +264,7 @@ struct Row {
   double outside;    // what of S lies outside the entries
 };
 
-// One warp: Write from the blocks' records, in lanes 0 to 15.  A gradient is a difference of terms, and 2^-24 of a
+// One warp: Write from the blocks' records, in the first `cluster` lanes, a power of two.  A gradient is a difference of terms, and 2^-24 of a
 // term is a rounding of what the larger one alone would give; the loss, a difference of larger terms, goes by row_of.
 __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int live, const Record* recs, int cluster,
                                           float tn_own) {
@@ -264,8 +272,7 @@ __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int liv
   const bool in = lane < cluster;
   const float own_n = in ? recs[lane].n : -INFINITY, own_tn = in ? recs[lane].tn : -INFINITY;
   float n = own_n, tn = own_tn, m = in ? recs[lane].m : -INFINITY;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = cluster / 2; o > 0; o >>= 1) {
     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
     tn = fmaxf(tn, __shfl_xor_sync(0xffffffffu, tn, o));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -273,8 +280,7 @@ __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int liv
   float s = own_n > -INFINITY ? (float)recs[lane].s * ex2(own_n - n) : 0.f;
   float ts = own_tn > -INFINITY ? (float)recs[lane].ts * ex2(own_tn - tn) : 0.f;
   float z = in ? (float)recs[lane].z : 0.f;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = cluster / 2; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     ts += __shfl_xor_sync(0xffffffffu, ts, o);
     z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -344,7 +350,7 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double m
   }
 }
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 8;  // of data, at most
 struct WarpSums {
   float s[kMaxWarps], n[kMaxWarps], m[kMaxWarps];
 };
@@ -363,19 +369,19 @@ __device__ __forceinline__ void give_warp(WarpSums& ws, const ExpSum& acc, float
     ws.s[threadIdx.x >> 5] = s;
   }
 }
-// One warp: the block's record, in lanes 0 to 15.
+// One warp: the block's record, in every lane.
 __device__ __forceinline__ Record block_record(const WarpSums& ws, int warps, const OwnSums& own) {
-  const int lane = threadIdx.x & 31;
-  const float mine = lane < warps ? ws.n[lane] : -INFINITY;
-  float n = mine, m = lane < warps ? ws.m[lane] : -INFINITY;
+  const int at = threadIdx.x % kMaxWarps;
+  const float mine = at < warps ? ws.n[at] : -INFINITY;
+  float n = mine, m = at < warps ? ws.m[at] : -INFINITY;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = kMaxWarps / 2; o > 0; o >>= 1) {
     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  double s = mine > -INFINITY ? (double)ws.s[lane] * pow2((double)mine - (double)n) : 0.0;
+  double s = mine > -INFINITY ? (double)ws.s[at] * pow2((double)mine - (double)n) : 0.0;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = kMaxWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return Record{s, own.ts, own.z, own.a, n, m, own.tn};
 }
 __device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const Record& t) {
@@ -389,17 +395,20 @@ __device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const 
 }
 
 // Marks: a word for each thread and tile, with a byte for each of its kVecs vectors there and a bit for each column
-// of an entry.  One warp clears those of `vecs` vectors and sets its block's entries'.
+// of an entry.  One warp clears those of `vecs` vectors, and sets its block's entries'.
 constexpr int kThreads = 256;
 constexpr int kPerSm = 4;         // blocks an SM
 constexpr int kData = kThreads - 32;
 constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
 constexpr int kTile = kData * kVecs;
 constexpr int kSlice = 40960;     // vectors of a slice at most: a byte of marks each
-template <int N>
-__device__ __forceinline__ void set_marks(uint32_t* marks, int first, int vecs, Own& own) {
-  for (int i = threadIdx.x & 31; i < (vecs + kTile - 1) / kTile * kData; i += 32) marks[i] = 0;
+__device__ __forceinline__ void clear_marks(uint32_t* marks, int vecs) {
+  for (int i = threadIdx.x & 31; i < (vecs + kTile - 1) / kTile * (kData / 4); i += 32)
+    reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
+}
+template <int N>
+__device__ __forceinline__ void set_marks(uint32_t* marks, int first, Own& own) {
   bool twice = false;
   for (int k = threadIdx.x & 31; k < own.n; k += 32) {
     const int vec = own.id[k] / N - first, tile = vec / kTile, at = vec % kTile;
@@ -538,8 +547,8 @@ struct Copies {
 // sum and one for the gradient (16 a clock and SM) take two thirds of the memory's time for bf16 in and out, half of
 // it for fp32.  The second read hits L2 while the rows in work take at most 48 MB, which the launch sees to with the
 // cluster's size: 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live rows have.  Measured
-// there: 123 us (584 MB, 4.8 TB/s); holding a row in registers or in shared memory between its sum and its gradient
-// took 231 and 346 us, for the work they leave to few threads; bringing the next rows into L2 meanwhile took 126.
+// there: 116 us (584 MB, 5.0 TB/s); holding a row in registers or in shared memory between its sum and its gradient
+// took 231 and 346 us, for the work they leave to few threads; bringing the next rows into L2 meanwhile was no faster.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   constexpr int N = Vec<T>::N;
@@ -561,6 +570,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   const int all = (d.V + N - 1) / N, per = (all + cluster - 1) / cluster;
   const int first = min((int)rank * per, all), last = min(first + per, all);
   const float w = d.row_weights ? d.row_weights[r] : 1.f;
+  Teacher in_row;
+  if (tid >= kData) {  // on their way together with the weight
+    read_teacher(d, r, in_row);
+    clear_marks(marks, last - first);
+  }
   const T* row = static_cast<const T*>(d.logits) + (size_t)r * d.ld;
   using Out = typename std::conditional<kGrad, G, float>::type;
   Out* out = kGrad ? static_cast<Out*>(a.grad) + (size_t)r * a.grad_ld : nullptr;
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     }
     return;
   }
-  cluster_arrive();  // all blocks have started before one stores into another
+  cluster_arrive_relaxed();  // all blocks have started before one stores into another
   if (tid < kData) {
     const uint4* const slice = reinterpret_cast<const uint4*>(row) + first;
     typename std::conditional<kGrad, Copies, Ahead>::type in;
@@ -608,8 +622,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     bar_arrive<2>(kThreads);  // sh.warps
     if (kGrad) in.template start<T>(slice, last - first, dynamic);
     cluster_wait();
-    cluster_arrive();
-    cluster_wait();
+    cluster_arrive_relaxed();
     if constexpr (kGrad) {
       bar_wait<1>(kThreads);  // sh.write
       const float n = sh.write.n, coef = sh.write.coef;
@@ -631,11 +644,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
       }
       bar_arrive<2>(kThreads);  // the entries' columns go over the others'
     }
+    cluster_wait();
     return;
   }
   const int lane = tid & 31;
-  find_own(a, r, first * N, last * N, sh.own, rank == 0);
-  set_marks<N>(marks, first, last - first, sh.own);
+  find_own(a, in_row, first * N, last * N, sh.own, rank == 0);
+  set_marks<N>(marks, first, sh.own);
   bar_wait<1>(kThreads);  // the marks are set
   sum_own(a, sh.own, row, sh.sums);
   bar_wait<2>(kThreads);  // sh.warps
@@ -699,7 +713,11 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
   int own_at = -1;  // the column of the thread's entry, where it is the first of its token's
   if (live) {
     for (int i = tid; i < kGradThreads * kGradVecs * N / 32; i += kGradThreads) bits[i] = 0;
-    if (tid < 32) find_own(a, r, first * N, min(first + kGradThreads * kGradVecs, all) * N, own, false);
+    if (tid < 32) {
+      Teacher in;
+      read_teacher(d, r, in);
+      find_own(a, in, first * N, min(first + kGradThreads * kGradVecs, all) * N, own, false);
+    }
     __syncthreads();
     bool again = false;
     if (tid < own.n) {
