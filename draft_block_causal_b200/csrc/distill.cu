@@ -30,6 +30,7 @@ constexpr int kEach = kMaxK / 32;  // entries a lane of the entries' warp
 struct DistillArgs {
   domino_distill_t d;
   float c;        // log2(e) / T
+  float c_rest;   // what its rounding left
   double inv_t;
   float* loss;
   float4* stats;  // two per row, see Stats
@@ -37,6 +38,7 @@ struct DistillArgs {
   void* grad;
   int64_t grad_ld;
   int cluster;    // blocks per row (k_distill_grad: chunks)
+  int in_work;    // rows in work at a time, about
   int32_t* status;
 };
 
@@ -100,6 +102,15 @@ __device__ __forceinline__ void read_teacher(const domino_distill_t& d, int r, T
       in.id[i] = __ldg(d.top_ids + (size_t)r * d.K + k);
       in.t[i] = __ldg(d.top_logits + (size_t)r * d.K + k);
     }
+  }
+}
+
+// Has a later row's entries brought into L2: under a full load of reads a miss takes 3000 cycles.
+__device__ __forceinline__ void await_teacher(const domino_distill_t& d, int r) {
+  for (int at = (threadIdx.x & 31) * 32; at < d.K + 31; at += 32 * 32) {
+    const size_t k = (size_t)r * d.K + min(at, d.K - 1);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(d.top_ids + k));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(d.top_logits + k));
   }
 }
 
@@ -287,7 +298,7 @@ __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int liv
   }
   const float psum = a.d.teacher_lse ? z : 1.f;
   const float rho = a.d.teacher_lse && s > 0.f ? fmaxf(0.f, 1.f - psum) : 0.f;
-  const float rest = s * ex2((float)(kLog2e * a.inv_t - (double)a.c) * big_clamp(m));  // c's rounding
+  const float rest = s * ex2(a.c_rest * big_clamp(m));
   Write o;
   o.n = n;
   o.live = live && (z > 0.f || isnan(z)) && (s > 0.f || ts > 0.f);
@@ -297,11 +308,11 @@ __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int liv
   const bool both = s > 0.f && ts > 0.f;
   const float gap = both ? tn - n : 0.f;
   const float all = ts * ex2(fminf(gap, 0.f)) + rest * ex2(fminf(-gap, 0.f));
-  const float outside = rest * ex2(fminf(-gap, 0.f)) / all;
-  o.coef = o.live && s > 0.f ? o.scale * (o.P * outside - rho) / s : 0.f;
+  const float outside = __fdividef(rest * ex2(fminf(-gap, 0.f)), all);  // all, s, z < 2^126: 2^-22 of a quotient
+  o.coef = o.live && s > 0.f ? __fdividef(o.scale * (o.P * outside - rho), s) : 0.f;
   o.guard = o.coef == 0.f || is_extreme(m);
-  o.of_e = ts > 0.f ? ex2(tn_own - (both ? fmaxf(tn, n) : tn)) / all : 0.f;
-  o.of_p = a.d.teacher_lse ? 1.f : 1.f / z;
+  o.of_e = ts > 0.f ? __fdividef(ex2(tn_own - (both ? fmaxf(tn, n) : tn)), all) : 0.f;
+  o.of_p = a.d.teacher_lse ? 1.f : __fdividef(1.f, z);
   return o;
 }
 
@@ -395,18 +406,13 @@ __device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const 
 }
 
 // Marks: a word for each thread and tile, with a byte for each of its kVecs vectors there and a bit for each column
-// of an entry.  One warp clears those of `vecs` vectors, and sets its block's entries'.
+// of an entry.  The threads clear their own, then one warp sets its block's entries'.
 constexpr int kThreads = 256;
 constexpr int kPerSm = 4;         // blocks an SM
 constexpr int kData = kThreads - 32;
 constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
 constexpr int kTile = kData * kVecs;
 constexpr int kSlice = 40960;     // vectors of a slice at most: a byte of marks each
-__device__ __forceinline__ void clear_marks(uint32_t* marks, int vecs) {
-  for (int i = threadIdx.x & 31; i < (vecs + kTile - 1) / kTile * (kData / 4); i += 32)
-    reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
-  __syncwarp();
-}
 template <int N>
 __device__ __forceinline__ void set_marks(uint32_t* marks, int first, Own& own) {
   bool twice = false;
@@ -573,7 +579,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   Teacher in_row;
   if (tid >= kData) {  // on their way together with the weight
     read_teacher(d, r, in_row);
-    clear_marks(marks, last - first);
+    if (rank == 0 && a.in_work < d.rows - r) await_teacher(d, r + a.in_work);
+  } else {
+    for (int i = 0; i < last - first; i += kTile) marks[i / kVecs + tid] = 0;
   }
   const T* row = static_cast<const T*>(d.logits) + (size_t)r * d.ld;
   using Out = typename std::conditional<kGrad, G, float>::type;
@@ -591,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   }
   cluster_arrive_relaxed();  // all blocks have started before one stores into another
   if (tid < kData) {
+    bar_arrive<2>(kThreads);  // the marks are clear
     const uint4* const slice = reinterpret_cast<const uint4*>(row) + first;
     typename std::conditional<kGrad, Copies, Ahead>::type in;
     in.template start<T>(slice, last - first, dynamic);
@@ -649,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   }
   const int lane = tid & 31;
   find_own(a, in_row, first * N, last * N, sh.own, rank == 0);
+  bar_wait<2>(kThreads);  // the marks are clear
   set_marks<N>(marks, first, sh.own);
   bar_wait<1>(kThreads);  // the marks are set
   sum_own(a, sh.own, row, sh.sums);
@@ -770,6 +780,7 @@ cudaError_t launch_distill(DistillArgs a, int grad_dtype, cudaStream_t st) {
            vecs / (2 * cluster) >= 2 * kData)))
     cluster *= 2;
   a.cluster = cluster;
+  a.in_work = (int)(blocks / cluster);
   const int smem = (a.grad ? kRing : 0) + ((vecs + cluster - 1) / cluster + kTile - 1) / kTile * kTile;
   const bool g = grad_dtype == DOMINO_DTYPE_F32;
   auto kern = !a.grad ? (f ? k_distill<float, void> : k_distill<bf16, void>)
@@ -826,7 +837,8 @@ DistillArgs make_args(const domino_distill_t& d, int32_t* status) {
   DistillArgs a{};
   a.d = d;
   a.inv_t = 1.0 / (double)d.temperature;
-  a.c = (float)(1.4426950408889634 * a.inv_t);
+  a.c = (float)(kLog2e * a.inv_t);
+  a.c_rest = (float)(kLog2e * a.inv_t - (double)a.c);
   a.status = status;
   return a;
 }
