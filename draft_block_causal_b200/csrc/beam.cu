@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(domino_beam_t p, in
   const float* const scores = p.scores + (size_t)g * p.W_in;
   const uint8_t* const finished = p.finished ? p.finished + (size_t)g * p.W_in : nullptr;
   const int all = (p.V + N - 1) / N, per = (all + parts - 1) / parts;
-  cluster_arrive();  // block 0 has started before another stores into it
+  cluster_arrive_relaxed();  // block 0 has started before another stores into it
   bool waited = false;
   for (int at = rank; at < givers; at += cluster) {  // once, or twice for more than 16 beams
     const int w = at / parts, part = at % parts;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_beam_select(domino_beam_t p, in
       uint32_t o = 0;
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
-        const int j = tid + i * kThreads;
+        const int j = slot(i);
         sc[i] = j < n ? sh.list[j] : 0;
         at[i] = j < n ? sh.from[j] : 0;
         o = max(o, order_bits(sc[i]));

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_top_rows(TopRows a, int cluster
   const uint32_t rank = blockIdx.x % cluster;
   if ((a.scores && !(a.scores[r] > -INFINITY)) || (a.finished && a.finished[r])) return;  // the whole cluster
   if (tid == 0) sh.count = sh.noted = 0;
-  if (cluster > 1) cluster_arrive();  // block 0 has started before another stores into it
+  if (cluster > 1) cluster_arrive_relaxed();  // block 0 has started before another stores into it
   const T* row = static_cast<const T*>(a.logits) + (size_t)r * a.ld;
   const int all = (a.V + N - 1) / N, per = (all + cluster - 1) / cluster;
   const int first = min((int)rank * per, all), last = min(first + per, all);
