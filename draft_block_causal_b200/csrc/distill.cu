@@ -275,8 +275,9 @@ struct Row {
   double outside;    // what of S lies outside the entries
 };
 
-// One warp: Write from the blocks' records, in the first `cluster` lanes, a power of two.  A gradient is a difference of terms, and 2^-24 of a
-// term is a rounding of what the larger one alone would give; the loss, a difference of larger terms, goes by row_of.
+// One warp: Write from the blocks' records, in the first `cluster` lanes, a power of two.  A gradient is a difference
+// of terms, and 2^-24 of a term is a rounding of what the larger one alone would give; the loss, a difference of
+// larger terms, goes by row_of.
 __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int live, const Record* recs, int cluster,
                                           float tn_own) {
   const int lane = threadIdx.x & 31;
@@ -410,6 +411,7 @@ __device__ __forceinline__ void send_record(Record* to_slot, uint32_t to, const 
 constexpr int kThreads = 256;
 constexpr int kPerSm = 4;         // blocks an SM
 constexpr int kData = kThreads - 32;
+static_assert(kData / 32 <= kMaxWarps, "a slot for each data warp");
 constexpr int kVecs = 4;          // 16-byte vectors a thread and tile
 constexpr int kTile = kData * kVecs;
 constexpr int kSlice = 40960;     // vectors of a slice at most: a byte of marks each
@@ -482,8 +484,9 @@ __device__ __forceinline__ void bar_wait(int n) {
 
 // A thread's own vectors of a slice, tile after tile.  Ahead in registers, one tile; or, for the gradient, by
 // asynchronous copies into its own places of shared memory, kStages - 1 tiles: no barrier is needed for either.
-// (Loss and gradient of 1024 rows of 151936 bf16: 136 us by registers, 127 by copies, 2 or 4 stages 130 and 147; the
-// loss alone of 512 rows fp32, whose larger slices' marks want the shared memory: 48 by registers and 57.)
+// (Loss and gradient of 1024 rows of 151936 bf16, when built: 136 us by registers, 127 by copies, 2 or 4 stages 130
+// and 147; the loss alone of 512 rows fp32, whose larger slices' marks want the shared memory: 48 by registers and
+// 57.)
 constexpr int kStages = 3;
 constexpr int kRing = kStages * kTile * 16;
 
@@ -553,7 +556,7 @@ struct Copies {
 // sum and one for the gradient (16 a clock and SM) take two thirds of the memory's time for bf16 in and out, half of
 // it for fp32.  The second read hits L2 while the rows in work take at most 48 MB, which the launch sees to with the
 // cluster's size: 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live rows have.  Measured
-// there: 116 us (584 MB, 5.0 TB/s); holding a row in registers or in shared memory between its sum and its gradient
+// there: 115 us (584 MB, 5.1 TB/s); holding a row in registers or in shared memory between its sum and its gradient
 // took 231 and 346 us, for the work they leave to few threads; bringing the next rows into L2 meanwhile was no faster.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {

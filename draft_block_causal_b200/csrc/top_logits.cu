@@ -3,9 +3,9 @@
 // A row is read once, by a cluster of blocks that take contiguous slices of it (top_scan.cuh).  Their candidates go
 // to block 0, with the sums, through distributed shared memory; block 0 cuts them and ranks what is left.
 //
-// Bound by memory: 512 rows of 151936 fp32 take 51 us for k = 8 (6.1 TB/s, 93% of the measured copy rate) and 58 us
+// Bound by memory: 512 rows of 151936 fp32 take 51 us for k = 8 (6.1 TB/s, 93% of the measured copy rate) and 59 us
 // for k = 64, whose notes and ranking come after all blocks' reads; bf16 rows by the exponentials as well, one a
-// value at 16 a clock and SM (1024 rows of 151936: 62 us, 5.0 TB/s).  One row of 151936 fp32 over 16 blocks: 9 us,
+// value at 16 a clock and SM (1024 rows of 151936: 62 us, 5.0 TB/s).  One row of 151936 fp32 over 16 blocks: 9.6 us,
 // all latency.
 #include "launch.cuh"
 #include "top_scan.cuh"

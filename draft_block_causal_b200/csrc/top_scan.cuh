@@ -304,7 +304,8 @@ __device__ __forceinline__ int scan_slice(const T* row, int first, int last, int
       }
     }
     if (can_bar) {
-      // not for two tiles or less: their notes cost less than the barriers (4000 rows of 32000 bf16, k = 8: 75 us for 81)
+      // not for two tiles or less: their notes cost less than the barriers (4000 rows of 32000 bf16, k = 8: 75 us
+      // for 81)
       if (stretch > 2 * kTile && (t0 >= last || last - t0 > 2 * kTile))
         bar = max(bar, reached_by(order_of(m), warps, k, sh));
       if (bar) floor = floor_at(bar + 1);
