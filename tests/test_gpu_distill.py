@@ -101,6 +101,17 @@ def test_random_rows(rows, V, K, dtype, tail):
     check(z, ids, val, lse if tail else None, weights=w, up=up)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,V,K", [(593, 2051, 128), (1300, 1504, 33), (160, 32003, 1)])
+def test_more_rows_than_run_at_once(rows, V, K, dtype):
+    g = torch.Generator().manual_seed(rows)
+    ids, val, lse = teacher(rows, V, K, 1.0, g)
+    z = R.padded((torch.randn(rows, V, generator=g) * 2.5).to(DT[dtype]))
+    w = torch.rand(rows, generator=g)
+    w[::7] = 0
+    check(z, ids, val, lse, weights=w.cuda())
+
+
 @pytest.mark.parametrize("tail", [False, True], ids=["entries", "rest"])
 @pytest.mark.parametrize("T", [0.25, 2.0, 31.0])
 def test_temperatures(T, tail):

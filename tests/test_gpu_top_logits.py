@@ -25,7 +25,7 @@ def check(logits, k, T=1.0):
     got = lse.double().cpu().numpy().reshape(-1)
     empty = want == -np.inf
     np.testing.assert_array_equal(got == -np.inf, empty)
-    err = np.abs(got - want)[~empty]
+    err = np.abs(got[~empty] - want[~empty])
     assert (err <= R.sum_tol(V) + 2.0 ** -23 * np.abs(want[~empty])).all(), err.max()
 
 
