@@ -93,13 +93,27 @@ __device__ __forceinline__ void raise(ExpSum& a, float n) {
   a.n = n;
 }
 
+// Whether any value of the vectors is NaN, where none is above -infinity: -infinities alone add up to one.
+template <typename T, int NV>
+__device__ __forceinline__ bool barred_by_nan(const uint4 (&q)[NV]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float z[Vec<T>::N];
+    widen(q[i], z);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; ++e) s += z[e];
+  }
+  return isnan(s);
+}
+
 // Adds the first `some` of the vectors, of maximum m (NaN aside), to a thread's sum; true where their terms need a
-// guard.  The reference is raised only when a term would exceed 2^kSlack of it, so that it hardly ever is after the
+// guard: a magnitude beyond kPlain or a NaN, of which the maximum of a tile without another value says nothing.  The reference is raised only when a term would exceed 2^kSlack of it, so that it hardly ever is after the
 // first vectors.
 constexpr float kSlack = 40.f;
 template <typename T, int NV>
 __device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], int some, float m, float c) {
-  if (!(m > -INFINITY)) return false;
+  if (!(m > -INFINITY)) return barred_by_nan<T>(q);
   if (fmaf(big_clamp(m), c, -a.n) > kSlack) raise(a, reference_of(m, c));
   float2 s = make_float2(0.f, 0.f);
   const float2 c2 = make_float2(c, c), n2 = make_float2(-a.n, -a.n);
