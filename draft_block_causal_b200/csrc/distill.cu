@@ -185,7 +185,10 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, co
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  const double to2 = a.inv_t * kLog2e, tn = most > -INFINITY ? ceil((double)big_clamp(most) * to2) : 0.0;
+  // a whole number that a float holds, as it is handed on in one: above 2^24 not every one is, and the reference may lie
+  // as far as 64 below the largest term's exponent (1e6 at T = 2^-10: 1.5e9), so that a term is 2^64 at most
+  const double to2 = a.inv_t * kLog2e;
+  const float tn = most > -INFINITY ? ceilf((float)((double)big_clamp(most) * to2)) : -INFINITY;
   double ts = 0.0, zs = 0.0, as = 0.0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -194,7 +197,7 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, co
     if (k >= n) break;
     const double y = own.y[k], x = (double)big_clamp(z[i]);
     const double pt = y > -INFINITY ? exp2_near((y - own.my) * kLog2e) : 0.0;
-    const double e = z[i] > -INFINITY ? exp2_near(x * to2 - tn) : 0.0;
+    const double e = z[i] > -INFINITY ? exp2_near(x * to2 - (double)tn) : 0.0;
     double p = pt;
     bool first = true;
     if (own.twice) {
@@ -218,7 +221,7 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, co
     as += __shfl_xor_sync(0xffffffffu, as, o);
   }
   if (lane == 0) {
-    sums.tn = most > -INFINITY ? (float)tn : -INFINITY;
+    sums.tn = tn;
     sums.ts = ts;
     sums.z = zs;
     sums.a = as;

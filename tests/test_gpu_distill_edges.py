@@ -1,6 +1,6 @@
-"""Distillation where single values decide: stretches of NaN logits.  Every call of `check` compares the loss alone, the
-fused gradient, the backward call and autograd with the fp64 definition, within the tolerances that test_gpu_distill
-derives."""
+"""Distillation where single values decide: stretches of NaN logits and references beyond 2^24.  Every call of
+`check` compares the loss alone, the fused gradient, the backward call and autograd with the fp64 definition, within the
+tolerances that test_gpu_distill derives."""
 import numpy as np
 import pytest
 import torch
@@ -68,3 +68,35 @@ def test_nan_in_more_rows_than_run_at_once():
     z[::2, 7200:] = np.nan
     z[1::2, :3600] = np.nan
     check(R.padded(z), ids, val, lse, grad_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("tail", [False, True], ids=["entries", "rest"])
+@pytest.mark.parametrize("T", [float(np.float32(0.05)), 2.0 ** -10])
+def test_references_beyond_24_bits(T, tail):
+    """log2(e) z / T of an entry above 2^24, where not every whole number is a float."""
+    rows, V, K = 24, 500, 5
+    g = torch.Generator().manual_seed(7)
+    # logits a few steps of T apart about a level at which the reference has more than 24 bits
+    level = 1.2 * 2 ** 24 * T / 1.4427 + 37.3 * T * torch.arange(rows)[:, None]
+    t = level + T * 2 * torch.randn(rows, V, generator=g)
+    val, ids = torch.topk(t.float(), K, dim=-1)
+    lse = torch.logsumexp(t.float().double() / T, -1).float().cuda()
+    z = level + T * 2 * torch.randn(rows, V, generator=g)
+    z[::3] = -level[::3] + T * torch.randn(rows, V, generator=g)[::3]
+    check(R.padded(z.float()), ids.int().cuda(), val.cuda(), lse if tail else None, T=T)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("K", [1, 3])
+@pytest.mark.parametrize("T", [float(np.float32(0.05)), 2.0 ** -10, float(np.float32(0.07))])
+def test_infinite_logit_at_an_entry(T, K, dtype):
+    g = torch.Generator().manual_seed(8)
+    z = torch.randn(4, 300, generator=g)
+    val, ids = torch.topk(torch.randn(4, 300, generator=g), K, dim=-1)
+    z[0, ids[0, 0]] = np.inf
+    z[1, ids[1]] = np.inf
+    z[2, ids[2, 0]] = 9e5
+    z[3, 17] = np.inf                      # ... as here, outside the entries
+    if K > 1:
+        val[0, 1:] = val[2, 1:] = -np.inf  # a positive mass there would cost 1e6 / T
+    check(R.padded(z.to(DT[dtype])), ids.int().cuda(), val.cuda(), None, T=T)
