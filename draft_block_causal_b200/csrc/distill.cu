@@ -295,6 +295,8 @@ __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int liv
   float s = own_n > -INFINITY ? (float)recs[lane].s * ex2(own_n - n) : 0.f;
   float ts = own_tn > -INFINITY ? (float)recs[lane].ts * ex2(own_tn - tn) : 0.f;
   float z = in ? (float)recs[lane].z : 0.f;
+  // a mass in 64 bits, as row_of sees it: fp32 has none below 2^-149
+  const bool mass = __any_sync(0xffffffffu, in && (recs[lane].z > 0.0 || isnan(recs[lane].z)));
   for (int o = cluster / 2; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     ts += __shfl_xor_sync(0xffffffffu, ts, o);
@@ -305,7 +307,7 @@ __device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int liv
   const float rest = s * ex2(a.c_rest * big_clamp(m));
   Write o;
   o.n = n;
-  o.live = live && (z > 0.f || isnan(z)) && (s > 0.f || ts > 0.f);
+  o.live = live && mass && (s > 0.f || ts > 0.f);
   o.scale = w * (float)a.inv_t;
   o.P = psum + rho;
   // S at the higher of the two references

@@ -1,6 +1,6 @@
-"""Distillation where single values decide: stretches of NaN logits and references beyond 2^24.  Every call of
-`check` compares the loss alone, the fused gradient, the backward call and autograd with the fp64 definition, within the
-tolerances that test_gpu_distill derives."""
+"""Distillation where single values decide: stretches of NaN logits, references beyond 2^24, and teachers whose
+entries hold next to nothing.  Every call of `check` compares the loss alone, the fused gradient, the backward call and
+autograd with the fp64 definition, within the tolerances that test_gpu_distill derives."""
 import numpy as np
 import pytest
 import torch
@@ -100,3 +100,23 @@ def test_infinite_logit_at_an_entry(T, K, dtype):
     if K > 1:
         val[0, 1:] = val[2, 1:] = -np.inf  # a positive mass there would cost 1e6 / T
     check(R.padded(z.to(DT[dtype])), ids.int().cuda(), val.cuda(), None, T=T)
+
+
+@pytest.mark.parametrize("below", [90.0, 104.0, 200.0, 600.0])
+def test_entries_far_below_the_teachers_sum(below):
+    """A positive mass that fp32 does not hold: loss and gradient are those of the rest of the vocabulary."""
+    rows, V, K = 4, 1000, 6
+    g = torch.Generator().manual_seed(9)
+    ids, val, lse = teacher(rows, V, K, 1.0, g)
+    z = torch.randn(rows, V, generator=g) * 2
+    check(R.padded(z), ids, val, (val[:, 0] + below).contiguous())
+    _, grad, _ = domino.distill(R.padded(z), ids, val, (val[:, 0] + below).contiguous(), grad_out=True)
+    assert (grad != 0).any(-1).all()
+
+
+def test_entries_far_below_at_a_low_temperature():
+    rows, V, K = 3, 700, 4
+    T = float(np.float32(0.05))
+    g = torch.Generator().manual_seed(10)
+    ids, val, lse = teacher(rows, V, K, T, g)
+    check(R.padded(torch.randn(rows, V, generator=g) * 0.1), ids, val, ((val[:, 0] + 5.5) / T).contiguous(), T=T)
