@@ -30,7 +30,6 @@ constexpr int kEach = kMaxK / 32;  // entries a lane of the entries' warp
 struct DistillArgs {
   domino_distill_t d;
   float c;        // log2(e) / T
-  float c_rest;   // what its rounding left
   double inv_t;
   float* loss;
   float4* stats;  // two per row, see Stats
@@ -75,13 +74,12 @@ struct Own {
   int twice;         // a token may be among them twice
   double my;         // what y is taken from: teacher_lse, or the row's largest y
   int32_t id[kMaxK];
-  double y[kMaxK];
+  double y[kMaxK];   // from sum_own on p = exp(y - my), all of the token's entries at its first, -1 at the others
 };
 
 // What one warp makes of them.
 struct OwnSums {
-  float e[kMaxK];    // 2^(log2(e) x - tn)
-  float p[kMaxK];    // exp(y - my), all of the token's entries at its first, -1 at the others
+  double e[kMaxK];   // 2^(log2(e) x - tn)
   float tn;
   double ts, z, a;   // as in Record
 };
@@ -156,21 +154,17 @@ __device__ __forceinline__ void find_own(const DistillArgs& a, Teacher& in, int 
   __syncwarp();
 }
 
-// 2^e of a whole number: 0 below 2^-1022, infinity above 2^1023.
-__device__ __forceinline__ double pow2(double e) {
-  const int n = (int)fmin(fmax(e, -1023.0), 1024.0);
+// 2^e of a whole number, in 64 bits: 0 below 2^-1022, infinity above 2^1023.  A difference of references is exact where
+// it lies between, as they are whole numbers.
+__device__ __forceinline__ double pow2(float e) {
+  const int n = (int)fminf(fmaxf(e, -1023.f), 1024.f);
   return __hiloint2double((n + 1023) << 20, 0);
 }
 
-// 2^t of a number in 64 bits: its whole part is exact, the rest goes through the fp32 exponential, 2^-22.
-__device__ __forceinline__ double exp2_near(double t) {
-  const double n = rint(t);
-  return (double)ex2((float)(t - n)) * pow2(n);
-}
-
-// One warp: the sums over a block's entries, from their logits in `row`.
+// One warp: the sums over a block's entries, from their logits in `row`.  In 64 bits: what a peaked teacher leaves to the
+// other tokens, one less the masses' sum, has no more digits than they have.
 template <typename T>
-__device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, const T* row, OwnSums& sums) {
+__device__ __forceinline__ void sum_own(const DistillArgs& a, Own& own, const T* row, OwnSums& sums) {
   const int lane = threadIdx.x & 31, n = own.n;
   float z[kEach], most = -INFINITY;
 #pragma unroll
@@ -196,22 +190,36 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, const Own& own, co
     const int k = 32 * i + lane;
     if (k >= n) break;
     const double y = own.y[k], x = (double)big_clamp(z[i]);
-    const double pt = y > -INFINITY ? exp2_near((y - own.my) * kLog2e) : 0.0;
-    const double e = z[i] > -INFINITY ? exp2_near(x * to2 - (double)tn) : 0.0;
-    double p = pt;
-    bool first = true;
-    if (own.twice) {
-      for (int j = 0; j < n; ++j)
-        if (own.id[j] == own.id[k] && j != k) {
-          first &= j > k;
-          if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - own.my) * kLog2e);
-        }
+    const double p = y > -INFINITY ? exp(y - own.my) : 0.0;
+    const double e = z[i] > -INFINITY ? exp2(x * to2 - (double)tn) : 0.0;
+    own.y[k] = p;
+    sums.e[k] = e;
+    if (!own.twice) ts += e;
+    zs += p;
+    if (p > 0.0) as += z[i] > -INFINITY ? p * (y - x * a.inv_t) : INFINITY;
+  }
+  __syncwarp();
+  if (own.twice) {  // a token's masses go to its first entry, and its term counts once
+    double all[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int k = 32 * i + lane;
+      if (k >= n) break;
+      all[i] = own.y[k];
+      for (int j = 0; j < n; ++j) {
+        if (own.id[j] != own.id[k] || j == k) continue;
+        if (j < k) all[i] = -1.0;
+        else if (all[i] >= 0.0) all[i] += own.y[j];
+      }
     }
-    sums.e[k] = (float)e;
-    sums.p[k] = first ? (float)p : -1.f;
-    if (first) ts += e;
-    zs += pt;
-    if (pt > 0.0) as += z[i] > -INFINITY ? pt * (y - x * a.inv_t) : INFINITY;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int k = 32 * i + lane;
+      if (k >= n) break;
+      own.y[k] = all[i];
+      if (all[i] >= 0.0) ts += sums.e[k];
+    }
   }
   __syncwarp();
 #pragma unroll
@@ -235,107 +243,64 @@ __device__ __forceinline__ double rounding_of_c(float m, float c, double inv_t) 
   return fabs(d) < 1e-5 ? 1.0 + d : exp(d);
 }
 
-// The blocks' records as the row's, by a whole warp, the result in lanes 0 to 15.
+// The blocks' records but for `a` as the row's, in every lane of a warp.
 __device__ __forceinline__ Record join_records(const Record* recs, int cluster) {
-  const int lane = threadIdx.x & 31;
-  Record t{0.0, 0.0, 0.0, 0.0, -INFINITY, -INFINITY, -INFINITY};
-  if (cluster == 1) return recs[0];
-  if (lane < cluster) t = recs[lane];
-  float n = t.n, tn = t.tn;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
-    tn = fmaxf(tn, __shfl_xor_sync(0xffffffffu, tn, o));
+  Record t = recs[threadIdx.x & (cluster - 1)];  // a power of two, at most 16
+  const float own_n = t.n, own_tn = t.tn;
+  for (int o = cluster / 2; o > 0; o >>= 1) {
+    t.n = fmaxf(t.n, __shfl_xor_sync(0xffffffffu, t.n, o));
+    t.tn = fmaxf(t.tn, __shfl_xor_sync(0xffffffffu, t.tn, o));
     t.m = fmaxf(t.m, __shfl_xor_sync(0xffffffffu, t.m, o));
   }
-  t.s = t.n > -INFINITY ? t.s * pow2((double)t.n - (double)n) : 0.0;
-  t.ts = t.tn > -INFINITY ? t.ts * pow2((double)t.tn - (double)tn) : 0.0;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  t.s = own_n > -INFINITY ? t.s * pow2(own_n - t.n) : 0.0;
+  t.ts = own_tn > -INFINITY ? t.ts * pow2(own_tn - t.tn) : 0.0;
+  for (int o = cluster / 2; o > 0; o >>= 1) {
     t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
     t.ts += __shfl_xor_sync(0xffffffffu, t.ts, o);
     t.z += __shfl_xor_sync(0xffffffffu, t.z, o);
-    t.a += __shfl_xor_sync(0xffffffffu, t.a, o);
   }
-  t.n = n;
-  t.tn = tn;
   return t;
 }
+__device__ __forceinline__ double join_a(const Record* recs, int cluster) {
+  double a = recs[threadIdx.x & (cluster - 1)].a;
+  for (int o = cluster / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
+}
 
-// What a block's gradient needs of a row, in fp32.
-struct Write {
-  float n, coef;     // a column that is no entry's: coef * 2^(c z - n)
-  int guard, live;
-  float scale, P;    // w / T; the teacher's mass
-  float of_e, of_p;  // an entry's: scale * (P * of_e * e - of_p * p)
-};
-// The same and more in 64 bits, for the loss and the stats.
+// What a row's loss, stats and gradient are made of.
 struct Row {
   int live;
-  double scale, P;
-  double zn;         // p = exp(y - my) / zn
-  double all;        // S * 2^-tn
-  double outside;    // what of S lies outside the entries
+  float top;           // reference of the next two
+  double total, rest;  // S and what of it lies outside the entries
+  double scale;        // w / T
+  double psum, rho;    // the teacher's mass on the entries and elsewhere, together P
 };
 
-// One warp: Write from the blocks' records, in the first `cluster` lanes, a power of two.  A gradient is a difference
-// of terms, and 2^-24 of a term is a rounding of what the larger one alone would give; the loss, a difference of
-// larger terms, goes by row_of.
-__device__ __forceinline__ Write write_of(const DistillArgs& a, float w, int live, const Record* recs, int cluster,
-                                          float tn_own) {
-  const int lane = threadIdx.x & 31;
-  const bool in = lane < cluster;
-  const float own_n = in ? recs[lane].n : -INFINITY, own_tn = in ? recs[lane].tn : -INFINITY;
-  float n = own_n, tn = own_tn, m = in ? recs[lane].m : -INFINITY;
-  for (int o = cluster / 2; o > 0; o >>= 1) {
-    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
-    tn = fmaxf(tn, __shfl_xor_sync(0xffffffffu, tn, o));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  }
-  float s = own_n > -INFINITY ? (float)recs[lane].s * ex2(own_n - n) : 0.f;
-  float ts = own_tn > -INFINITY ? (float)recs[lane].ts * ex2(own_tn - tn) : 0.f;
-  float z = in ? (float)recs[lane].z : 0.f;
-  // a mass in 64 bits, as row_of sees it: fp32 has none below 2^-149
-  const bool mass = __any_sync(0xffffffffu, in && (recs[lane].z > 0.0 || isnan(recs[lane].z)));
-  for (int o = cluster / 2; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    ts += __shfl_xor_sync(0xffffffffu, ts, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
-  const float psum = a.d.teacher_lse ? z : 1.f;
-  const float rho = a.d.teacher_lse && s > 0.f ? fmaxf(0.f, 1.f - psum) : 0.f;
-  const float rest = s * ex2(a.c_rest * big_clamp(m));
-  Write o;
-  o.n = n;
-  o.live = live && mass && (s > 0.f || ts > 0.f);
-  o.scale = w * (float)a.inv_t;
-  o.P = psum + rho;
-  // S at the higher of the two references
-  const bool both = s > 0.f && ts > 0.f;
-  const float gap = both ? tn - n : 0.f;
-  const float all = ts * ex2(fminf(gap, 0.f)) + rest * ex2(fminf(-gap, 0.f));
-  const float outside = __fdividef(rest * ex2(fminf(-gap, 0.f)), all);  // all, s, z < 2^126: 2^-22 of a quotient
-  o.coef = o.live && s > 0.f ? __fdividef(o.scale * (o.P * outside - rho), s) : 0.f;
-  o.guard = o.coef == 0.f || is_extreme(m);
-  o.of_e = ts > 0.f ? __fdividef(ex2(tn_own - (both ? fmaxf(tn, n) : tn)), all) : 0.f;
-  o.of_p = a.d.teacher_lse ? 1.f : __fdividef(1.f, z);
+__device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, const Record& t) {
+  Row o;
+  o.live = live && (t.z > 0.0 || isnan(t.z)) && (t.s > 0.0 || t.ts > 0.0);
+  o.top = t.ts > 0.0 ? (t.s > 0.0 ? fmaxf(t.n, t.tn) : t.tn) : t.n;
+  o.rest = t.s > 0.0 ? t.s * rounding_of_c(t.m, a.c, a.inv_t) * pow2(t.n - o.top) : 0.0;
+  o.total = o.rest + (t.ts > 0.0 ? t.ts * pow2(t.tn - o.top) : 0.0);
+  o.scale = (double)w * a.inv_t;
+  o.psum = a.d.teacher_lse ? t.z : 1.0;
+  o.rho = a.d.teacher_lse && t.s > 0.0 ? fmax(0.0, 1.0 - o.psum) : 0.0;
   return o;
 }
 
-__device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, const Record& t) {
-  Row o{};
-  const double rest = t.s * rounding_of_c(t.m, a.c, a.inv_t);
-  o.live = live && (t.z > 0.0 || isnan(t.z)) && (t.s > 0.0 || t.ts > 0.0);
-  o.zn = a.d.teacher_lse ? 1.0 : t.z;
-  const double psum = a.d.teacher_lse ? t.z : 1.0;
-  const double rho = a.d.teacher_lse && t.s > 0.0 ? fmax(0.0, 1.0 - psum) : 0.0;
-  o.scale = (double)w * a.inv_t;
-  o.P = psum + rho;
-  const double gap = (double)t.n - (double)t.tn;  // infinite where one of them is
-  o.outside = t.ts > 0.0 ? rest / (rest + t.ts * pow2(-gap)) : 1.0;
-  o.all = t.ts + (t.s > 0.0 ? rest * pow2(gap) : 0.0);
-  return o;
+// The factor of 2^(c z - n) in the gradient of a column that is no entry's: scale (P tau - rho) / s.  In 64 bits, as rho
+// is, up to its rounding: rho has no more digits than the masses that it is one less the sum of, and the difference is
+// small for a student close to its teacher.
+__device__ __forceinline__ float coef_of(const Record& t, const Row& o) {
+  if (!o.live || !(t.s > 0.0)) return 0.f;
+  return (float)(o.scale * ((o.psum + o.rho) * o.rest - o.rho * o.total) / (o.total * t.s));
 }
+
+// What the data warps' gradient needs of a row: coef * 2^(c z - n) at a column that is no entry's.
+struct Write {
+  float n, coef;
+  int guard;
+};
 
 // Loss and stats of a row: one thread of block 0.
 __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double my, const Record& t, const Row& o) {
@@ -344,22 +309,21 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int r, double m
     store_stats(a.stats, r, Stats{});
     return;
   }
-  // L from the entries' reference unless the others' sum is beyond it; log tau = log outside unless that is too small
-  const bool from_top = t.ts > 0.0 && o.all < 1e300;
-  const double l_rest = !from_top || o.outside < 1e-300 ? log_sum_exp(t.s, t.n, t.m, a.c, a.inv_t) : 0.0;
-  const double L = from_top ? kLn2 * (log2(o.all) + (double)t.tn) : l_rest;
-  const double lp = a.d.teacher_lse ? my : my + log(t.z);
-  const double psum = a.d.teacher_lse ? t.z : 1.0, rho = o.P - psum;
-  const double of_rho = o.outside < 1e-300 ? log(rho) - l_rest + L : log(rho / o.outside);
-  const double loss = t.a / o.zn - psum * lp + psum * L + (rho > 0.0 ? rho * of_rho : 0.0);
+  const double L = kLn2 * (log2(o.total) + (double)o.top);
+  const double lp = a.d.teacher_lse ? my : my + log(t.z), zn = a.d.teacher_lse ? 1.0 : t.z;
+  double loss = t.a / zn - o.psum * lp + o.psum * L;
+  if (o.rho > 0.0) {  // log tau = log(rest / total) unless that is too small
+    const double tau = o.rest / o.total;
+    loss += o.rho * (tau < 1e-300 ? log(o.rho) - log_sum_exp(t.s, t.n, t.m, a.c, a.inv_t) + L : log(o.rho / tau));
+  }
   a.loss[r] = (float)(o.scale / a.inv_t * loss);
   if (a.stats) {
     Stats st;
     st.n = t.n;
-    st.rest = t.s > 0.0 ? (float)(o.scale * (o.P * o.outside - rho) / t.s) : 0.f;
+    st.rest = coef_of(t, o);
     st.l_hi = (float)L;
     st.l_lo = (float)(L - (double)st.l_hi);
-    st.all = (float)(o.scale * o.P);
+    st.all = (float)(o.scale * (o.psum + o.rho));
     st.scale = (float)o.scale;
     st.lp_hi = (float)lp;
     st.lp_lo = (float)(lp - (double)st.lp_hi);
@@ -396,7 +360,7 @@ __device__ __forceinline__ Record block_record(const WarpSums& ws, int warps, co
     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  double s = mine > -INFINITY ? (double)ws.s[at] * pow2((double)mine - (double)n) : 0.0;
+  double s = mine > -INFINITY ? (double)ws.s[at] * pow2(mine - n) : 0.0;
 #pragma unroll
   for (int o = kMaxWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return Record{s, own.ts, own.z, own.a, n, m, own.tn};
@@ -574,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
     WarpSums warps;
     Write write;
   } sh;
-  extern __shared__ __align__(16) char dynamic[];  // the copies' places, then the marks
+  // the copies' places, then the marks; a place that does not start on 32 bytes costs (130 us for 116 with 16 off)
+  extern __shared__ __align__(128) char dynamic[];
   uint32_t* const marks = reinterpret_cast<uint32_t*>(dynamic + (kGrad ? kRing : 0));
   pdl_wait();
   pdl_trigger();
@@ -678,24 +643,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   cluster_arrive();
   cluster_wait();
   if (!kGrad && rank != 0) return;
+  Record t = join_records(sh.recs, cluster);
+  const Row o = row_of(a, w, sh.own.live, t);
   if constexpr (kGrad) {
-    const Write o = write_of(a, w, sh.own.live, sh.recs, cluster, sh.sums.tn);
-    if (lane == 0) sh.write = o;
+    const float coef = coef_of(t, o);
+    if (lane == 0) sh.write = Write{t.n, coef, coef == 0.f || is_extreme(t.m)};
     bar_wait<1>(kThreads);  // sh.write
   }
   if (rank == 0) {
-    const Record t = join_records(sh.recs, cluster);
-    if (lane == 0) finish_row(a, r, sh.own.my, t, row_of(a, w, sh.own.live, t));
+    t.a = join_a(sh.recs, cluster);
+    if (lane == 0) finish_row(a, r, sh.own.my, t, o);
   }
   if constexpr (kGrad) {
+    // an entry's: scale * (P q - p)
+    const double of_e = t.ts > 0.0 ? o.scale * (o.psum + o.rho) * pow2(sh.sums.tn - o.top) / o.total : 0.0;
+    const double of_p = d.teacher_lse ? o.scale : o.scale / t.z;
     bar_wait<2>(kThreads);
-    const Write& o = sh.write;
     if (o.live)
       for (int k = lane; k < sh.own.n; k += 32)
-        if (sh.sums.p[k] >= 0.f) {
-          const float q_v = sh.sums.e[k] > 0.f ? sh.sums.e[k] * o.of_e : 0.f;
-          store_grad(out + sh.own.id[k], o.scale * (o.P * q_v - sh.sums.p[k] * o.of_p));
-        }
+        if (sh.own.y[k] >= 0.0) store_grad(out + sh.own.id[k], (float)(of_e * sh.sums.e[k] - of_p * sh.own.y[k]));
   }
 }
 
@@ -727,8 +693,9 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
     const int vec = first + i * kGradThreads + tid;
     q[i] = live && vec < all ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : barred_vec<T>();
   }
-  float own_grad = 0.f;
-  int own_at = -1;  // the column of the thread's entry, where it is the first of its token's
+  float own_z = 0.f;
+  int own_at = -1;  // the column of the thread's entry
+  bool twice = false;
   if (live) {
     for (int i = tid; i < kGradThreads * kGradVecs * N / 32; i += kGradThreads) bits[i] = 0;
     if (tid < 32) {
@@ -740,33 +707,33 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
     bool again = false;
     if (tid < own.n) {
       own_at = own.id[tid];
+      own_z = to_f32(row[own_at]);
       const int at = own_at - first * N;
       const uint32_t bit = 1u << (at & 31);
       again = (atomicOr(&bits[at >> 5], bit) & bit) != 0;
     }
-    const bool twice = __syncthreads_or(again);
-    if (own_at >= 0) {
-      const double lp = (double)st.lp_hi + (double)st.lp_lo, L = (double)st.l_hi + (double)st.l_lo;
-      const float z = to_f32(row[own_at]);
-      double p = own.y[tid] > -INFINITY ? exp2_near((own.y[tid] - lp) * kLog2e) : 0.0;
-      const double q_v = z > -INFINITY ? exp2_near(((double)big_clamp(z) * a.inv_t - L) * kLog2e) : 0.0;
-      if (twice) {
-        for (int j = 0; j < own.n; ++j)
-          if (own.id[j] == own.id[tid] && j != tid) {
-            if (own.y[j] > -INFINITY) p += exp2_near((own.y[j] - lp) * kLog2e);
-            if (j < tid) own_at = -1;
-          }
-      }
-      own_grad = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
-    }
+    twice = __syncthreads_or(again);  // the entries' logits are read, too
   }
-  __syncthreads();  // the entries' logits are read
   const float coef = live ? g * st.rest : 0.f;
   const bool guard = coef == 0.f || is_extreme(st.n / a.c);
 #pragma unroll
   for (int i = 0; i < kGradVecs; ++i) {
     const int vec = first + i * kGradThreads + tid;
     if (vec < all) write_vector<T, true>(out + vec * N, d.V - vec * N, q[i], a.c, st.n, coef, guard);
+  }
+  float own_grad = 0.f;
+  if (own_at >= 0) {  // in 64 bits, as in k_distill, while the vectors are on their way
+    const double lp = (double)st.lp_hi + (double)st.lp_lo, L = (double)st.l_hi + (double)st.l_lo;
+    double p = own.y[tid] > -INFINITY ? exp(own.y[tid] - lp) : 0.0;
+    const double q_v = own_z > -INFINITY ? exp((double)big_clamp(own_z) * a.inv_t - L) : 0.0;
+    if (twice) {
+      for (int j = 0; j < own.n; ++j)
+        if (own.id[j] == own.id[tid] && j != tid) {
+          if (own.y[j] > -INFINITY) p += exp(own.y[j] - lp);
+          if (j < tid) own_at = -1;  // the token's first entry writes
+        }
+    }
+    own_grad = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
   }
   __syncthreads();
   if (own_at >= 0) store_grad(out + own_at, own_grad);
@@ -846,7 +813,6 @@ DistillArgs make_args(const domino_distill_t& d, int32_t* status) {
   a.d = d;
   a.inv_t = 1.0 / (double)d.temperature;
   a.c = (float)(kLog2e * a.inv_t);
-  a.c_rest = (float)(kLog2e * a.inv_t - (double)a.c);
   a.status = status;
   return a;
 }
