@@ -861,25 +861,59 @@ def distill_backward(logits, top_ids, top_logits, stats, grad_loss=None, teacher
     return grad_out
 
 
+def _saved(t, name: str, n: int, dtype, device):
+    """``t`` that autograd saved, of n values, contiguous and from a 16-byte boundary on: itself, or a copy where a
+    saved-tensor hook has laid it out anew."""
+    if t is None:
+        return t
+    if t.dtype is not dtype or t.numel() != n or t.device != device:
+        raise ValueError(f"saved {name} came back with {t.numel()} values of {t.dtype} on {t.device}, expected {n} of "
+                         f"{dtype} on {device}")
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _saved_rows(logits):
+    """``logits`` that autograd saved, in rows as the library takes them, with what _logit_rows says of them: a
+    saved-tensor hook may have laid them out anew (rows without their padding), and then they are copied."""
+    try:
+        rows = _logit_rows(logits, "logits")
+        if logits.data_ptr() % 16 == 0:
+            return logits, rows
+    except ValueError:
+        pass  # of another layout: its shape and type are the forward call's
+    copy = _new_rows(logits, logits.shape[:-1], logits.shape[-1], None).copy_(logits)
+    return copy, _logit_rows(copy, "logits")
+
+
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status):
         loss, _, stats = distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status=status)
         ctx.save_for_backward(logits, top_ids, top_logits, teacher_lse, row_weights, stats)
-        ctx.temperature = temperature
+        ctx.temperature, ctx.size = temperature, (loss.numel(), logits.shape, top_ids.shape[-1], logits.dtype)
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
-        # the arguments were checked in forward; what is saved may come back elsewhere, but alike
+        # the arguments were checked in forward; a saved-tensor hook may give them back in another place and layout
         logits, top_ids, top_logits, teacher_lse, row_weights, stats = ctx.saved_tensors
-        lead, V, ld, code = _logit_rows(logits, "logits")
-        dev = logits.device
+        dev, (rows, shape, K, dtype) = grad_loss.device, ctx.size
+        if logits.shape != shape or logits.dtype is not dtype or logits.device != dev:
+            raise ValueError(f"saved logits came back as {tuple(logits.shape)} of {logits.dtype} on {logits.device}, "
+                             f"expected {tuple(shape)} of {dtype} on {dev}")
+        logits, (lead, V, ld, code) = _saved_rows(logits)
+        top_ids = _saved(top_ids, "top_ids", rows * K, torch.int32, dev)
+        top_logits = _saved(top_logits, "top_logits", rows * K, torch.float32, dev)
+        teacher_lse = _saved(teacher_lse, "teacher_lse", rows, torch.float32, dev)
+        row_weights = _saved(row_weights, "row_weights", rows, torch.float32, dev)
+        stats = _saved(stats, "stats", rows * 8, torch.float32, dev)
         if not grad_loss.is_contiguous():
             grad_loss = grad_loss.contiguous()
         grad = _new_rows(logits, lead, V, None)
-        a = DistillArgs(stats.numel() // 8, V, ld, code, top_ids.shape[-1], logits.data_ptr(), top_ids.data_ptr(),
+        a = DistillArgs(rows, V, ld, code, K, logits.data_ptr(), top_ids.data_ptr(),
                         top_logits.data_ptr(), _data(teacher_lse), _data(row_weights), ctx.temperature)
         rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(), grad_loss.data_ptr(),
                      grad.data_ptr(), (V + 7) // 8 * 8, code, None, _raw_stream(None, dev))
