@@ -670,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
 // read theirs first.  Bound by memory: forward and backward of 360 rows of 50001 bf16 take 30 us of GPU time together
 // for 104 MB, of which the two kernels' starts and the entries' chains of loads are a third.
 constexpr int kGradThreads = 256;
+static_assert(kGradThreads >= kMaxK, "a thread an entry");
 constexpr int kGradVecs = 8;
 
 template <typename T, typename G>
@@ -734,6 +735,11 @@ __global__ void __launch_bounds__(kGradThreads, 4) k_distill_grad(DistillArgs a)
         }
     }
     own_grad = (float)((double)g * (q_v * (double)st.all - p * (double)st.scale));
+  }
+  // a bad id of a row that is read, one without a gradient too: by the row's first block
+  if (a.status && chunk == 0 && tid < d.K && g != 0.f && !(d.row_weights && d.row_weights[r] == 0.f)) {
+    const int32_t id = __ldg(d.top_ids + (size_t)r * d.K + tid);
+    if (id < -1 || id >= d.V) set_status(a.status, DOMINO_STATUS_BAD_TOKEN);
   }
   __syncthreads();
   if (own_at >= 0) store_grad(out + own_at, own_grad);

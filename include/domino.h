@@ -328,8 +328,9 @@ DOMINO_API int domino_beam_select(const domino_beam_t* beam, void* workspace, si
  * a row without student mass, without an entry of positive mass (or with teacher_lse not finite): loss and
  * gradient are 0.  Where the student has no mass outside the entries the term of the other tokens is
  * left out.  A student that bars an entry of positive mass has loss +infinity.  Entries: id -1 is no
- * entry (rows may have fewer than K); any other id outside [0, V) sets DOMINO_STATUS_BAD_TOKEN and is
- * taken as none; a token given twice counts with both its masses, each a term of the sum.
+ * entry (rows may have fewer than K); any other id outside [0, V) in a row that is read sets
+ * DOMINO_STATUS_BAD_TOKEN, in both calls, and is taken as none; a token given twice counts with both its
+ * masses, each a term of the sum.
  *   top_ids [rows, K] int32, top_logits [rows, K] fp32, 1 <= K <= DOMINO_MAX_TOP; teacher_lse and
  *   row_weights [rows] fp32 or NULL.
  *

@@ -1,4 +1,5 @@
-"""distill_loss with the tensors that it saves: laid out anew by a saved-tensor hook."""
+"""distill_loss with the tensors that it saves: laid out anew by a saved-tensor hook; and the status word of the
+backward call."""
 import pytest
 import torch
 
@@ -53,3 +54,37 @@ def test_saved_tensors_of_another_type_size_or_device_are_refused(pack, dtype):
     with pytest.raises(ValueError, match="came back"):
         loss.sum().backward()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("V,K", [(600, 5), (151936, 128)])
+def test_the_backward_call_reports_bad_tokens(V, K):
+    z, ids, val, lse = inputs(4, V, K)
+    for bad in (V, -2, 2 ** 31 - 1):
+        bad_ids, ok_ids = ids.clone(), ids.clone()
+        bad_ids[2, K - 1], ok_ids[2, K - 1] = bad, -1
+        _, _, stats = domino.distill(z, ok_ids, val, lse)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        want = domino.distill_backward(z, ok_ids, val, stats, teacher_lse=lse, status=status)
+        assert int(status.item()) == 0
+        got = domino.distill_backward(z, bad_ids, val, stats, teacher_lse=lse, status=status)
+        assert int(status.item()) == domino.STATUS_BAD_TOKEN and torch.equal(got, want)
+        domino.distill_backward(z, bad_ids, val, stats, teacher_lse=lse)  # without a status word
+        # a row that has no gradient for want of an entry reports as the forward call does
+        bad_ids[2] = bad
+        for call in ("forward", "backward"):
+            status.zero_()
+            if call == "forward":
+                _, _, stats = domino.distill(z, bad_ids, val, status=status)
+            else:
+                domino.distill_backward(z, bad_ids, val, stats, status=status)
+            assert int(status.item()) == domino.STATUS_BAD_TOKEN
+        # rows that are not read report nothing
+        w, up = torch.ones(4, device="cuda"), torch.ones(4, device="cuda")
+        w[2] = 0.0
+        status.zero_()
+        _, _, stats = domino.distill(z, bad_ids, val, row_weights=w, status=status)
+        domino.distill_backward(z, bad_ids, val, stats, row_weights=w, status=status)
+        up[2] = 0.0
+        _, _, stats = domino.distill(z, bad_ids, val)
+        domino.distill_backward(z, bad_ids, val, stats, up, status=status)
+        assert int(status.item()) == 0
