@@ -231,6 +231,13 @@ def _expect(t, name: str, shape, dtype, device) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _expect_out(t, name: str, shape, dtype, device) -> None:
+    """_expect for a tensor that the call fills.  Autograd is told, as by torch's operations in place: a backward pass
+    that has saved the tensor is then refused, where it would compute with what the call left there."""
+    _expect(t, name, shape, dtype, device)
+    torch._C._increment_version((t,))
+
+
 def _expect_status(status, device) -> None:
     if status is not None:
         if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.numel() < 1:
@@ -427,11 +434,11 @@ def alloc_workspace(nbytes: int, device=None) -> torch.Tensor:
 
 
 def _check_greedy_outputs(tokens_out, logits_out, states_out, B, L, Hs, V, dev) -> None:
-    _expect(tokens_out, "tokens_out", (B, L), torch.int32, dev)
+    _expect_out(tokens_out, "tokens_out", (B, L), torch.int32, dev)
     if logits_out is not None:
-        _expect(logits_out, "logits_out", (B, L, V), torch.float32, dev)
+        _expect_out(logits_out, "logits_out", (B, L, V), torch.float32, dev)
     if states_out is not None:
-        _expect(states_out, "states_out", (B, L, Hs), torch.float32, dev)
+        _expect_out(states_out, "states_out", (B, L, Hs), torch.float32, dev)
 
 
 def draft_greedy(w: HeadWeights, base_logits, hidden, S0, tokens_out=None, logits_out=None, states_out=None,
@@ -506,13 +513,13 @@ def teacher_forced(w: HeadWeights, base_logits, hidden, S0, tokens, logits_out=N
     _expect(tokens, "tokens", (B, L), torch.int32, dev)
     if logits_out is None:
         logits_out = torch.empty((B, L, V), dtype=logits_dtype, device=dev)
-    _expect(logits_out, "logits_out", (B, L, V), (torch.float32, torch.bfloat16), dev)
+    _expect_out(logits_out, "logits_out", (B, L, V), (torch.float32, torch.bfloat16), dev)
     if states_out is True:
         states_out = torch.empty((B, L, Hs), dtype=torch.float32, device=dev)
     if states_out is False:
         states_out = None
     if states_out is not None:
-        _expect(states_out, "states_out", (B, L, Hs), torch.float32, dev)
+        _expect_out(states_out, "states_out", (B, L, Hs), torch.float32, dev)
     _expect_status(status, dev)
     sh = make_shape(w, B, L)
     if workspace is None:
@@ -675,15 +682,15 @@ def top_logits(logits, k: int, temperature: float = 1.0, values_out=None, ids_ou
     if values_out is None:
         values_out = _new(logits, lead + (k,), torch.float32, stream)
     else:
-        _expect(values_out, "values_out", lead + (k,), torch.float32, dev)
+        _expect_out(values_out, "values_out", lead + (k,), torch.float32, dev)
     if ids_out is None:
         ids_out = _new(logits, lead + (k,), torch.int32, stream)
     else:
-        _expect(ids_out, "ids_out", lead + (k,), torch.int32, dev)
+        _expect_out(ids_out, "ids_out", lead + (k,), torch.int32, dev)
     if lse_out is None:
         lse_out = _new(values_out, lead, torch.float32, stream)
     else:
-        _expect(lse_out, "lse_out", lead, torch.float32, dev)
+        _expect_out(lse_out, "lse_out", lead, torch.float32, dev)
     rc = _launch(dev, lib().domino_top_logits, logits.numel() // V, V, ld, code, logits.data_ptr(), k,
                  float(temperature), values_out.data_ptr(), ids_out.data_ptr(), lse_out.data_ptr(), sp)
     _check(rc, "domino_top_logits")
@@ -746,18 +753,18 @@ def beam_select(logits, scores, beams: int, states=None, history=None, pos: int 
                        None if history is None else _new(history, (B, n, hist_len), torch.int32, stream),
                        None if eos < 0 else _new(scores, (B, n), torch.uint8, stream))
     else:
-        _expect(out.scores, "out.scores", (B, n), torch.float32, dev)
-        _expect(out.parents, "out.parents", (B, n), torch.int32, dev)
-        _expect(out.tokens, "out.tokens", (B, n), torch.int32, dev)
+        _expect_out(out.scores, "out.scores", (B, n), torch.float32, dev)
+        _expect_out(out.parents, "out.parents", (B, n), torch.int32, dev)
+        _expect_out(out.tokens, "out.tokens", (B, n), torch.int32, dev)
         for name, given, dims, dt in (("states", states, (B, n, Hs), torch.float32),
                                       ("history", history, (B, n, hist_len), torch.int32)):
             t = getattr(out, name)
             if (t is None) != (given is None):
                 raise ValueError(f"out.{name} must be given exactly when {name} is")
             if t is not None:
-                _expect(t, f"out.{name}", dims, dt, dev)
+                _expect_out(t, f"out.{name}", dims, dt, dev)
         if out.finished is not None:
-            _expect(out.finished, "out.finished", (B, n), torch.uint8, dev)
+            _expect_out(out.finished, "out.finished", (B, n), torch.uint8, dev)
     nbytes = 0
     if workspace is None:
         nbytes = lib().domino_beam_workspace_bytes(B, W, n, V, code)
@@ -800,6 +807,7 @@ def _expect_grad(grad, lead, V, dev):
         raise ValueError(f"grad_out has shape {tuple(grad.shape)}, expected {tuple(lead) + (V,)}")
     if grad.device != dev:
         raise ValueError(f"grad_out is on {grad.device}, expected {dev}")
+    torch._C._increment_version((grad,))  # as _expect_out
     return gld, gcode
 
 
@@ -822,13 +830,13 @@ def distill(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 
     if loss_out is None:
         loss_out = _new(top_logits, lead, torch.float32, stream)
     else:
-        _expect(loss_out, "loss_out", lead, torch.float32, dev)
+        _expect_out(loss_out, "loss_out", lead, torch.float32, dev)
     if stats_out is None and grad_out is None or stats_out is True:
         stats_out = _new(top_logits, lead + (8,), torch.float32, stream)
     elif stats_out is False:
         stats_out = None
     elif stats_out is not None:
-        _expect(stats_out, "stats_out", lead + (8,), torch.float32, dev)
+        _expect_out(stats_out, "stats_out", lead + (8,), torch.float32, dev)
     _expect_status(status, dev)
     gld = gcode = 0
     if grad_out is not None:

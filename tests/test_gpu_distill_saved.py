@@ -1,13 +1,18 @@
-"""distill_loss with the tensors that it saves: laid out anew by a saved-tensor hook; and the status word of the
-backward call."""
+"""distill_loss with the tensors it saves: laid out anew by a hook, or overwritten before the backward pass; and the
+status word of the backward call."""
 import pytest
 import torch
 
-from draft_block_causal_b200 import domino
+from draft_block_causal_b200 import domino, synth
 from tests import rows_reference as R
 from tests.test_gpu_distill import DT, teacher
 
 pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from tests import gpu_common as G
+else:
+    G = None
 
 
 def inputs(rows, V, K, dtype="fp32", seed=0):
@@ -53,6 +58,61 @@ def test_saved_tensors_of_another_type_size_or_device_are_refused(pack, dtype):
         loss = domino.distill_loss(x, ids, val, lse)
     with pytest.raises(ValueError, match="came back"):
         loss.sum().backward()
+    torch.cuda.synchronize()
+
+
+def test_a_call_that_fills_a_saved_tensor_is_seen_by_autograd():
+    """An output buffer that holds what an earlier loss has saved: its backward pass is refused, as after a torch
+    operation in place."""
+    z, ids, val, lse = inputs(6, 1200, 5)
+    x = z.detach().requires_grad_()
+    top = domino.top_logits(z, 5)
+    loss = domino.distill_loss(x, top[1], top[0], top[2])
+    domino.top_logits(-z, 5, values_out=top[0], ids_out=top[1], lse_out=top[2])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    for call in (lambda y: domino.distill(y, ids, val, lse, grad_out=y),
+                 lambda y: domino.distill_backward(y, ids, val, stats, teacher_lse=lse, grad_out=y)):
+        _, _, stats = domino.distill(z, ids, val, lse)
+        y = z.clone()
+        loss = domino.distill_loss(y.view(6, 1200).requires_grad_() * 1.0, ids, val, lse)
+        loss.sum().backward()               # its own logits are untouched
+        z1 = z.clone().requires_grad_() * 1.0
+        loss = domino.distill_loss(z1, ids, val, lse)
+        call(z1.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.sum().backward()
+    # one entry a row: [6, 1] is as large as the losses of 6 rows and the scores of 2 x 3 beams
+    one, first = ids[:, :1].contiguous(), val[:, :1].contiguous()
+    loss = domino.distill_loss(x, one, first)
+    domino.distill(z, ids, val, lse, loss_out=first.view(6))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    first = val[:, :1].contiguous()
+    loss = domino.distill_loss(x, one, first)
+    beams = domino.beam_select(z.view(2, 3, 1200), torch.zeros(2, 3, device="cuda"), 3)
+    domino.beam_select(z.view(2, 3, 1200), torch.zeros(2, 3, device="cuda"), 3,
+                       out=beams._replace(scores=first.view(2, 3)))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    # the head's logits, refilled by its next call
+    data = synth.make_workload(dict(B=2, L=3, d=128, Hs=64, r=64, V=1000, dtype=synth.BF16, weight_seed=1, input_seed=2,
+                                    s0_std=0.1, peak=2.0, name="saved"), with_tokens=True)
+    w, lb, h, S0 = G.device_inputs(data)
+    toks = torch.from_numpy(data["tokens"]).cuda()
+    logits, states = domino.teacher_forced(w, lb, h, S0, toks, states_out=True)
+    top = domino.top_logits(lb, 5)
+    for refill in (lambda: domino.teacher_forced(w, lb, h, S0, toks, logits_out=logits),
+                   lambda: domino.draft_greedy(w, lb, h, S0, logits_out=logits)):
+        bias = torch.zeros(1000, device="cuda", requires_grad=True)
+        (bias * logits).sum().backward()    # in time
+        loss = (bias * logits).sum() + domino.distill_loss(logits + bias, top[1], top[0], top[2]).sum()
+        refill()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():            # no versions there
+        top = domino.top_logits(z, 5)
+        domino.top_logits(z, 5, values_out=top[0], ids_out=top[1], lse_out=top[2])
     torch.cuda.synchronize()
 
 
