@@ -822,6 +822,13 @@ def distill(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 
     (0: the row is skipped).  ``grad_out``: True for a gradient in the logits' type, or a tensor (fp32 or bf16) to
     fill, which may be ``logits`` itself; it is the gradient of the sum of the losses.  ``stats`` goes to
     ``distill_backward``: made when no gradient is asked for, or with ``stats_out`` (True, or a tensor to fill)."""
+    return _distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, grad_out, loss_out, stats_out,
+                    status, stream)[:3]
+
+
+def _distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, grad_out, loss_out, stats_out, status,
+             stream):
+    """distill, with the row stride of the logits."""
     a, lead, V = _distill_args(logits, top_ids, top_logits, teacher_lse, temperature, row_weights)
     dev = logits.device
     sp = _raw_stream(stream, dev)
@@ -846,7 +853,7 @@ def distill(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 
     rc = _launch(dev, lib().domino_distill, ctypes.byref(a), loss_out.data_ptr(), _data(stats_out),
                  _data(grad_out), gld, gcode, _data(status), sp)
     _check(rc, "domino_distill")
-    return loss_out, grad_out, stats_out
+    return loss_out, grad_out, stats_out, a.ld
 
 
 def distill_backward(logits, top_ids, top_logits, stats, grad_loss=None, teacher_lse=None, temperature: float = 1.0,
@@ -870,59 +877,55 @@ def distill_backward(logits, top_ids, top_logits, stats, grad_loss=None, teacher
 
 
 def _saved(t, name: str, n: int, dtype, device):
-    """``t`` that autograd saved, of n values, contiguous and from a 16-byte boundary on: itself, or a copy where a
-    saved-tensor hook has laid it out anew."""
-    if t is None:
-        return t
+    """``t`` that autograd saved, of n values: itself, or an aligned contiguous copy where a saved-tensor hook has laid
+    it out anew."""
     if t.dtype is not dtype or t.numel() != n or t.device != device:
         raise ValueError(f"saved {name} came back with {t.numel()} values of {t.dtype} on {t.device}, expected {n} of "
                          f"{dtype} on {device}")
-    if t.is_contiguous() and t.data_ptr() % 16 == 0:
-        return t
-    return t.clone(memory_format=torch.contiguous_format)
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
-def _saved_rows(logits):
-    """``logits`` that autograd saved, in rows as the library takes them, with what _logit_rows says of them: a
-    saved-tensor hook may have laid them out anew (rows without their padding), and then they are copied."""
-    try:
-        rows = _logit_rows(logits, "logits")
-        if logits.data_ptr() % 16 == 0:
-            return logits, rows
-    except ValueError:
-        pass  # of another layout: its shape and type are the forward call's
-    copy = _new_rows(logits, logits.shape[:-1], logits.shape[-1], None).copy_(logits)
-    return copy, _logit_rows(copy, "logits")
+def _saved_rows(logits, strides, ld):
+    """``logits`` that autograd saved, in rows as the library takes them, and their row stride: what they had in the
+    forward call.  A saved-tensor hook may have laid them out anew (rows without their padding): then they are copied."""
+    V = logits.shape[-1]
+    if logits.stride() == strides and logits.data_ptr() % 16 == 0 and (
+            V % 8 == 0 or (logits.storage_offset() + (logits.numel() // V - 1) * ld + (V + 7) // 8 * 8)
+            * logits.element_size() <= logits.untyped_storage().nbytes()):
+        return logits, ld
+    logits = _new_rows(logits, logits.shape[:-1], V, None).copy_(logits)
+    return logits, (V + 7) // 8 * 8
 
 
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status):
-        loss, _, stats = distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status=status)
-        ctx.save_for_backward(logits, top_ids, top_logits, teacher_lse, row_weights, stats)
-        ctx.temperature, ctx.size = temperature, (loss.numel(), logits.shape, top_ids.shape[-1], logits.dtype)
+        loss, _, stats, ld = _distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, None, None, None,
+                                      status, None)
+        ctx.save_for_backward(logits, top_ids, top_logits, stats)  # stats hold what the others are read for
+        ctx.given = temperature, logits.shape, logits.stride(), ld, logits.dtype, top_ids.numel()
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
         # the arguments were checked in forward; a saved-tensor hook may give them back in another place and layout
-        logits, top_ids, top_logits, teacher_lse, row_weights, stats = ctx.saved_tensors
-        dev, (rows, shape, K, dtype) = grad_loss.device, ctx.size
+        logits, top_ids, top_logits, stats = ctx.saved_tensors
+        temperature, shape, strides, ld, dtype, entries = ctx.given
+        dev, rows = grad_loss.device, grad_loss.numel()
         if logits.shape != shape or logits.dtype is not dtype or logits.device != dev:
             raise ValueError(f"saved logits came back as {tuple(logits.shape)} of {logits.dtype} on {logits.device}, "
                              f"expected {tuple(shape)} of {dtype} on {dev}")
-        logits, (lead, V, ld, code) = _saved_rows(logits)
-        top_ids = _saved(top_ids, "top_ids", rows * K, torch.int32, dev)
-        top_logits = _saved(top_logits, "top_logits", rows * K, torch.float32, dev)
-        teacher_lse = _saved(teacher_lse, "teacher_lse", rows, torch.float32, dev)
-        row_weights = _saved(row_weights, "row_weights", rows, torch.float32, dev)
+        logits, ld = _saved_rows(logits, strides, ld)
+        top_ids = _saved(top_ids, "top_ids", entries, torch.int32, dev)
+        top_logits = _saved(top_logits, "top_logits", entries, torch.float32, dev)
         stats = _saved(stats, "stats", rows * 8, torch.float32, dev)
         if not grad_loss.is_contiguous():
             grad_loss = grad_loss.contiguous()
-        grad = _new_rows(logits, lead, V, None)
-        a = DistillArgs(rows, V, ld, code, K, logits.data_ptr(), top_ids.data_ptr(),
-                        top_logits.data_ptr(), _data(teacher_lse), _data(row_weights), ctx.temperature)
+        V, code = shape[-1], _DTYPE_CODE[dtype]
+        grad = _new_rows(logits, shape[:-1], V, None)
+        a = DistillArgs(rows, V, ld, code, entries // rows, logits.data_ptr(), top_ids.data_ptr(),
+                        top_logits.data_ptr(), None, None, temperature)
         rc = _launch(dev, lib().domino_distill_backward, ctypes.byref(a), stats.data_ptr(), grad_loss.data_ptr(),
                      grad.data_ptr(), (V + 7) // 8 * 8, code, None, _raw_stream(None, dev))
         _check(rc, "domino_distill_backward")

@@ -339,8 +339,8 @@ DOMINO_API int domino_beam_select(const domino_beam_t* beam, void* workspace, si
  *   values grad_ld apart (a multiple of 8, >= V, 16-byte aligned base) in grad_dtype, rounded once;
  *   columns from V on are left as they were.
  * domino_distill_backward: the gradient of sum_r grad_loss[r] * loss[r] (grad_loss NULL: 1) from the
- *   same arguments and the stats that domino_distill wrote for them; a row whose grad_loss is 0 is not
- *   read and its gradient is 0.
+ *   same arguments and the stats that domino_distill wrote for them, which hold what teacher_lse and
+ *   row_weights say (both may be NULL here); a row whose grad_loss is 0 is not read and its gradient is 0.
  * grad may be the logits themselves (same ld and dtype); outputs may not overlap inputs or each other
  * otherwise (DOMINO_ERR_INVALID_ARGUMENT). */
 typedef struct {

@@ -95,6 +95,13 @@ def test_a_call_that_fills_a_saved_tensor_is_seen_by_autograd():
                        out=beams._replace(scores=first.view(2, 3)))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.sum().backward()
+    # row weights and the teacher's log-sum-exp are read by the forward call alone
+    w, row = torch.rand(6, device="cuda"), lse.clone()
+    want = torch.autograd.grad(domino.distill_loss(x, ids, val, row, row_weights=w).sum(), x)[0]
+    loss = domino.distill_loss(x, ids, val, row, row_weights=w)
+    domino.top_logits(z, 5, lse_out=w)
+    row.zero_()
+    assert torch.equal(torch.autograd.grad(loss.sum(), x)[0], want)
     # the head's logits, refilled by its next call
     data = synth.make_workload(dict(B=2, L=3, d=128, Hs=64, r=64, V=1000, dtype=synth.BF16, weight_seed=1, input_seed=2,
                                     s0_std=0.1, peak=2.0, name="saved"), with_tokens=True)
