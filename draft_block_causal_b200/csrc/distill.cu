@@ -5,8 +5,8 @@
 // and its gradient   w / T * (P exp(x_v - L) - p_v)  at an entry's token,
 //                    w / T * (P exp(L_rest - L) - rho) * exp(x_v - L_rest)  elsewhere.
 // The row is summed without the entries' columns, about its own reference, and the at most 128 entries' terms
-// are added in 64 bits: S_rest as S less the entries' terms would be lost for a student that puts all but 1e-7 of
-// its mass on them.  log p_k is y_k less the entries' log-sum, so the entries need one exponential each.
+// are formed and added in 64 bits: S_rest as S less the entries' terms would be lost for a student that puts all but 1e-7
+// of its mass on them, and so would rho, one less the sum of p, with masses in fp32 for such a teacher.  log p_k is y_k less the entries' log-sum, so the entries need one exponential each.
 //
 // A cluster of blocks takes a row (k_distill): each sums its slice, they exchange sums through distributed shared
 // memory, and for the gradient each reads its slice again, out of L2, and writes.  A block deals with the entries
@@ -524,9 +524,12 @@ struct Copies {
 // Bound by memory, then by the exponentials: V values are read once from DRAM and V written; one exponential for the
 // sum and one for the gradient (16 a clock and SM) take two thirds of the memory's time for bf16 in and out, half of
 // it for fp32.  The second read hits L2 while the rows in work take at most 48 MB, which the launch sees to with the
-// cluster's size: 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live rows have.  Measured
-// there: 115 us (584 MB, 5.1 TB/s); holding a row in registers or in shared memory between its sum and its gradient
-// took 231 and 346 us, for the work they leave to few threads; bringing the next rows into L2 meanwhile was no faster.
+// cluster's size as far as 16 blocks a row will do (up to 340,000 fp32 or 680,000 bf16 a row; at 2^20 fp32 they are
+// 155 MB, more than L2 holds): 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live
+// rows have.  Measured there: 117 us (584 MB, 5.0 TB/s; 128 when calls of it in a row bring the power limit's 1.77 GHz);
+// holding a row in registers or in shared memory between its sum and its gradient took 231 and 346 us, for the work
+// they leave to few threads; bringing the next rows into L2 meanwhile was no faster.  The entries and the row's factors
+// in 64 bits take 1 of the 117 us.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   constexpr int N = Vec<T>::N;
