@@ -4,9 +4,10 @@
 // row's loss is   w * (sum_k p_k (log p_k - x_k + L) + rho (log rho - L_rest + L))
 // and its gradient   w / T * (P exp(x_v - L) - p_v)  at an entry's token,
 //                    w / T * (P exp(L_rest - L) - rho) * exp(x_v - L_rest)  elsewhere.
-// The row is summed without the entries' columns, about its own reference, and the at most 128 entries' terms
-// are formed and added in 64 bits: S_rest as S less the entries' terms would be lost for a student that puts all but 1e-7
-// of its mass on them, and so would rho, one less the sum of p, with masses in fp32 for such a teacher.  log p_k is y_k less the entries' log-sum, so the entries need one exponential each.
+// The row is summed without the entries' columns, about its own reference, and the at most 128 entries' terms are
+// formed and added in 64 bits: S_rest as S less the entries' terms would be lost for a student that puts all but
+// 1e-7 of its mass on them, and so would rho, one less the sum of p, with masses in fp32 for such a teacher.  log
+// p_k is y_k less the entries' log-sum, so the entries need one exponential each.
 //
 // A cluster of blocks takes a row (k_distill): each sums its slice, they exchange sums through distributed shared
 // memory, and for the gradient each reads its slice again, out of L2, and writes.  A block deals with the entries
@@ -161,8 +162,8 @@ __device__ __forceinline__ double pow2(float e) {
   return __hiloint2double((n + 1023) << 20, 0);
 }
 
-// One warp: the sums over a block's entries, from their logits in `row`.  In 64 bits: what a peaked teacher leaves to the
-// other tokens, one less the masses' sum, has no more digits than they have.
+// One warp: the sums over a block's entries, from their logits in `row`.  In 64 bits: what a peaked teacher leaves to
+// the other tokens, one less the masses' sum, has no more digits than they have.
 template <typename T>
 __device__ __forceinline__ void sum_own(const DistillArgs& a, Own& own, const T* row, OwnSums& sums) {
   const int lane = threadIdx.x & 31, n = own.n;
@@ -179,8 +180,8 @@ __device__ __forceinline__ void sum_own(const DistillArgs& a, Own& own, const T*
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // a whole number that a float holds, as it is handed on in one: above 2^24 not every one is, and the reference may lie
-  // as far as 64 below the largest term's exponent (1e6 at T = 2^-10: 1.5e9), so that a term is 2^64 at most
+  // a whole number that a float holds, as it is handed on in one: above 2^24 not every one is, and the reference may
+  // lie as far as 64 below the largest term's exponent (1e6 at T = 2^-10: 1.5e9), so that a term is 2^64 at most
   const double to2 = a.inv_t * kLog2e;
   const float tn = most > -INFINITY ? ceilf((float)((double)big_clamp(most) * to2)) : -INFINITY;
   double ts = 0.0, zs = 0.0, as = 0.0;
@@ -288,9 +289,9 @@ __device__ __forceinline__ Row row_of(const DistillArgs& a, float w, int live, c
   return o;
 }
 
-// The factor of 2^(c z - n) in the gradient of a column that is no entry's: scale (P tau - rho) / s.  In 64 bits, as rho
-// is, up to its rounding: rho has no more digits than the masses that it is one less the sum of, and the difference is
-// small for a student close to its teacher.
+// The factor of 2^(c z - n) in the gradient of a column that is no entry's: scale (P tau - rho) / s.  In 64 bits, as
+// rho is, up to its rounding: rho has no more digits than the masses that it is one less the sum of, and the
+// difference is small for a student close to its teacher.
 __device__ __forceinline__ float coef_of(const Record& t, const Row& o) {
   if (!o.live || !(t.s > 0.0)) return 0.f;
   return (float)(o.scale * ((o.psum + o.rho) * o.rest - o.rho * o.total) / (o.total * t.s));
@@ -525,11 +526,11 @@ struct Copies {
 // sum and one for the gradient (16 a clock and SM) take two thirds of the memory's time for bf16 in and out, half of
 // it for fp32.  The second read hits L2 while the rows in work take at most 48 MB, which the launch sees to with the
 // cluster's size as far as 16 blocks a row will do (up to 340,000 fp32 or 680,000 bf16 a row; at 2^20 fp32 they are
-// 155 MB, more than L2 holds): 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live
-// rows have.  Measured there: 117 us (584 MB, 5.0 TB/s; 128 when calls of it in a row bring the power limit's 1.77 GHz);
+// 155 MB, more than L2 holds): 1024 rows of 151936 bf16 read 275 MB of DRAM for the 272 MB that their live rows
+// have.  Measured there: 117 us (584 MB, 5.0 TB/s; 128 when calls of it in a row bring the power limit's 1.77 GHz);
 // holding a row in registers or in shared memory between its sum and its gradient took 231 and 346 us, for the work
-// they leave to few threads; bringing the next rows into L2 meanwhile was no faster.  The entries and the row's factors
-// in 64 bits take 1 of the 117 us.
+// they leave to few threads; bringing the next rows into L2 meanwhile was no faster.  The entries and the row's
+// factors in 64 bits take 1 of the 117 us.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_distill(DistillArgs a) {
   constexpr int N = Vec<T>::N;

@@ -108,8 +108,8 @@ __device__ __forceinline__ bool barred_by_nan(const uint4 (&q)[NV]) {
 }
 
 // Adds the first `some` of the vectors, of maximum m (NaN aside), to a thread's sum; true where their terms need a
-// guard: a magnitude beyond kPlain or a NaN, of which the maximum of a tile without another value says nothing.  The reference is raised only when a term would exceed 2^kSlack of it, so that it hardly ever is after the
-// first vectors.
+// guard: a magnitude beyond kPlain or a NaN, of which the maximum of a tile without another value says nothing.  The
+// reference is raised only when a term would exceed 2^kSlack of it, so that it hardly ever is after the first vectors.
 constexpr float kSlack = 40.f;
 template <typename T, int NV>
 __device__ __forceinline__ bool add_vectors(ExpSum& a, const uint4 (&q)[NV], int some, float m, float c) {

@@ -887,7 +887,7 @@ def _saved(t, name: str, n: int, dtype, device):
 
 def _saved_rows(logits, strides, ld):
     """``logits`` that autograd saved, in rows as the library takes them, and their row stride: what they had in the
-    forward call.  A saved-tensor hook may have laid them out anew (rows without their padding): then they are copied."""
+    forward call.  A saved-tensor hook may have laid them out anew (rows without padding); they are copied then."""
     V = logits.shape[-1]
     if logits.stride() == strides and logits.data_ptr() % 16 == 0 and (
             V % 8 == 0 or (logits.storage_offset() + (logits.numel() // V - 1) * ld + (V + 7) // 8 * 8)
@@ -900,8 +900,8 @@ def _saved_rows(logits, strides, ld):
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_ids, top_logits, teacher_lse, temperature, row_weights, status):
-        loss, _, stats, ld = _distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, None, None, None,
-                                      status, None)
+        loss, _, stats, ld = _distill(logits, top_ids, top_logits, teacher_lse, temperature, row_weights, None, None,
+                                      None, status, None)
         ctx.save_for_backward(logits, top_ids, top_logits, stats)  # stats hold what the others are read for
         ctx.given = temperature, logits.shape, logits.stride(), ld, logits.dtype, top_ids.numel()
         return loss
@@ -935,7 +935,8 @@ class _DistillLoss(torch.autograd.Function):
 def distill_loss(logits, top_ids, top_logits, teacher_lse=None, temperature: float = 1.0, row_weights=None,
                  status=None):
     """``distill``'s loss as a differentiable function of ``logits``, on the current stream: [...] fp32, one per row.
-    The teacher's tensors and the row weights are constants: one that requires a gradient is refused.  To capture a
+    The teacher's tensors and the row weights are constants: one that requires a gradient is refused.  A call that fills
+    the logits or the entries before the backward pass makes that raise, as an operation in place does.  To capture a
     step with its backward pass into a CUDA graph, run it once on the capturing stream first and drop what earlier
     steps of the same leaves have returned: their nodes belong to another stream."""
     for name, t in (("top_logits", top_logits), ("teacher_lse", teacher_lse), ("row_weights", row_weights)):
